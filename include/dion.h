@@ -56,7 +56,8 @@ typedef enum dion_status {
   DION_ERR_NOT_INITIALIZED = 5,     /* null or freed handle                       */
   DION_ERR_DEVICE = 6,              /* current device is not sm_100 (B200)       */
   DION_ERR_MISALIGNED = 7,          /* a device pointer is not aligned as required
-                                       (16 bytes for the Dion step, 4 for dion_vec_step) */
+                                       (16 bytes for the Dion step, 4 for dion_vec_step,
+                                       an element for rows)                        */
   DION_ERR_HOST = 8                 /* host-side failure (out of host memory); no C++
                                        exception ever leaves the library             */
 } dion_status;
@@ -437,6 +438,195 @@ dion_status dion_vec_step(const dion_vec_tensor* tensors, int32_t ntensors,
 
 /* Kernel launches made by the most recent dion_vec_step on this thread. */
 int32_t dion_vec_last_launch_count(void);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Where the gradients come from.  The step reads G of the 2-D weights, the vector step g
+ * of the gains, biases and tables; the entry points below compute them in the form that
+ * is read (fp32), next to the forward passes that they belong to.  Common to all:
+ *  - arrays [tokens, features] are row-major with rows `ld*` elements apart (ld >=
+ *    features); rows that start on 16 bytes with features % 8 == 0 take a vectorised
+ *    path.  Rows past `tokens` and columns past `features` are neither read nor written.
+ *  - tokens may be 0.  Gains and gradients of gains are contiguous fp32 arrays.
+ *  - arguments are checked before anything is enqueued; the work is enqueued on `stream`
+ *    of the current device, and the call returns.  No entry point allocates device memory
+ *    or synchronises.  A workspace needs no clearing and no keeping between calls, and must
+ *    not be shared by two calls in flight.
+ *  - `accumulate` != 0 adds to the gradient that is there (a further micro-batch);
+ *    0 overwrites it.
+ *  - results repeat bit for bit: no sum is taken by floating-point atomics.
+ */
+typedef enum dion_dtype { DION_BF16 = 0, DION_FP16 = 1, DION_FP32 = 2 } dion_dtype;
+
+/*
+ * Activations in 8 bits: a block of DION_ACT_BLOCK features of one token is e4m3 bytes q_i
+ * and a byte E, standing for q_i 2^(E - 127).  The exponent is the smallest with
+ * max |x_i| <= 448 * 2^(E - 127) (448 is e4m3's largest value), kept within [10, 246];
+ * values are rounded to nearest even (2^-4 relative, or 2^-10 * 2^(E - 127) for a block's
+ * smallest values).  A block that holds a NaN or an infinity has E = 255 and reads as NaN.
+ * Every other value is exact in bf16.
+ */
+#define DION_ACT_BLOCK 32
+typedef struct dion_act_kept {
+  uint8_t* q;      /* [tokens, ld], ld = features rounded up to DION_ACT_BLOCK; 16-byte
+                      aligned; the padding columns are written as zeros                 */
+  uint8_t* scale;  /* [tokens, ld / DION_ACT_BLOCK]                                     */
+  int64_t tokens, features;
+} dion_act_kept;
+
+/* x [tokens, features] (dtype: dion_dtype) into kept, and kept back into x.  fp16 output
+ * overflows to infinity where the value exceeds fp16's range. */
+dion_status dion_act_save(const void* x, int64_t ldx, int32_t dtype, const dion_act_kept* kept,
+                          void* stream);
+dion_status dion_act_load(const dion_act_kept* kept, void* x, int64_t ldx, int32_t dtype,
+                          void* stream);
+
+/*
+ * The gradient of a weight from its layer's kept input A (tokens x m = features) and its
+ * output's gradient D (tokens x n, bf16), in fp32:
+ *     G (m x n) = A^T D,     or, where `transposed`,     G (n x m) = D^T A
+ * (the first for y = x W, the second for y = x W^T).  A NaN in A or D makes the entries
+ * that it meets NaN.  m and n at most 2^24.
+ */
+typedef struct dion_grad_source {
+  dion_act_kept kept;
+  const void* d;       /* bf16 [tokens, n]; rows that do not start on 16 bytes are copied
+                          into the workspace first                                      */
+  int64_t ldd, n;
+  float* G;            /* rows ldg elements apart                                       */
+  int64_t ldg;
+  int32_t transposed;
+} dion_grad_source;
+
+/* Bytes of workspace for a list of sources (they take turns in it); 0 when none is needed
+ * or the sources are invalid. */
+size_t dion_weight_grad_workspace(const dion_grad_source* sources, int32_t nsources);
+
+/* Every gradient of the list, one after the other.  d_status (may be NULL): device int32,
+ * one word per source, into which DION_MAT_TIMEOUT is OR-ed where a bounded device wait
+ * ran out (that gradient is then not valid). */
+dion_status dion_weight_grad(const dion_grad_source* sources, int32_t nsources, int32_t accumulate,
+                             void* d_workspace, size_t workspace_bytes, int32_t* d_status,
+                             void* stream);
+
+/*
+ * dion_step_batched with the gradients formed from kept activations: sources[i] belongs to
+ * matrix i (bucket by bucket, slot by slot) and its gradient is written to that matrix's
+ * slot of ptrs[b].G (which this call therefore overwrites; the sources' own G and ldg are
+ * not read).  Each source must have the matrix's shape: features x n, or n x features where
+ * transposed.  `accumulate` != 0 adds to what ptrs[b].G holds (the earlier micro-batches).
+ * grad_status (may be NULL) is dion_weight_grad's d_status.  The workspace must have
+ * dion_step_from_saved_workspace bytes.
+ */
+size_t dion_step_from_saved_workspace(dion_handle h, const dion_grad_source* sources,
+                                      int32_t nsources);
+dion_status dion_step_batched_from_saved(dion_handle h, const dion_bucket_ptrs* ptrs,
+                                         const dion_grad_source* sources, int32_t nbuckets,
+                                         int32_t accumulate, float lr, void* d_workspace,
+                                         size_t workspace_bytes, int32_t* d_status,
+                                         int32_t* grad_status, void* stream);
+
+/*
+ * The norms around a block, fused with the block's gate and residual scale.  With
+ * rms(v) = 1 / sqrt(mean(v^2) + eps) over the features of a token, x the residual stream
+ * and y the block's output:
+ *     h = x + residual_scale gate * z,   z = post_gain * y rms(y)   (z = y without post_norm)
+ *     u = pre_gain * h rms(h)
+ * Gains and gate are per feature (NULL: ones).  Without y, h = x is not written and u is
+ * the plain pre-norm; without u only the residual is updated.  Arithmetic is fp32, each
+ * output is rounded once (u from the unrounded h).  `kept`, when given, receives u in 8
+ * bits, from the unrounded u.  h may be x, and u may be x or y (same rows); no other
+ * overlap.  features <= 16384.  Rows whose sum of squares overflows fp32 are not supported.
+ */
+typedef struct dion_norm {
+  int64_t tokens, features;
+  int32_t dtype;          /* dion_dtype of x, y, h, u                                   */
+  int32_t post_norm;      /* 1: y is normalised                                         */
+  float eps;              /* > 0                                                        */
+  float residual_scale;
+  const void* x;
+  int64_t ldx;
+  const void* y;          /* may be NULL                                                */
+  int64_t ldy;
+  void* h;                /* may be NULL                                                */
+  int64_t ldh;
+  void* u;                /* may be NULL                                                */
+  int64_t ldu;
+  const float *pre_gain, *post_gain, *gate;
+  const dion_act_kept* kept;  /* may be NULL                                            */
+} dion_norm;
+
+dion_status dion_norm_forward(const dion_norm* args, void* stream);
+
+/*
+ * Its gradients at the stored h and y.  du, dh: gradients of u and of h from elsewhere (at
+ * least one); dx: of x; the others of what they are named after.  Every output may be NULL.
+ * h is read only where du is given (it is x where the forward pass had no y).  dx may be dh,
+ * du or h, dy may be y or du (same rows); no other overlap.
+ */
+typedef struct dion_norm_grad {
+  int64_t tokens, features;
+  int32_t dtype, post_norm;
+  float eps, residual_scale;
+  const void* h;
+  int64_t ldh;
+  const void* y;
+  int64_t ldy;
+  const void* du;
+  int64_t lddu;
+  const void* dh;
+  int64_t lddh;
+  void* dx;
+  int64_t lddx;
+  void* dy;
+  int64_t lddy;
+  const float *pre_gain, *post_gain, *gate;
+  float *dpre_gain, *dpost_gain, *dgate;
+  int32_t accumulate;     /* of dpre_gain, dpost_gain and dgate                         */
+} dion_norm_grad;
+
+size_t dion_norm_backward_workspace(int64_t tokens, int64_t features);
+dion_status dion_norm_backward(const dion_norm_grad* args, void* d_workspace,
+                               size_t workspace_bytes, void* stream);
+
+/*
+ * Embedding lookup with scaling, out[t] = scale * table[ids[t]], and the table's gradient,
+ *     dtable[v] (+)= scale * sum over t with ids[t] = v of dout[t]
+ * (fp32; every row of dtable is written, rows without a token as zeros; with `accumulate`
+ * those are left alone).  ids are int32 or int64; an id outside [0, vocab) stands for no
+ * token: its row of out is zero and its row of dout is not read.  Rows of one token are added
+ * in the order of their positions, in pieces.  vocab <= 2^31 - 2, features <= 2^24.
+ */
+typedef struct dion_embed {
+  int64_t tokens, vocab, features;
+  const void* ids;
+  int32_t id_bytes;       /* 4 or 8                                                     */
+  int32_t table_dtype, out_dtype;
+  float scale;
+  const void* table;      /* [vocab, features], rows ldt apart                          */
+  int64_t ldt;
+  void* out;              /* [tokens, features], rows ldo apart                         */
+  int64_t ldo;
+} dion_embed;
+
+dion_status dion_embed_lookup(const dion_embed* args, void* stream);
+
+typedef struct dion_embed_grad {
+  int64_t tokens, vocab, features;
+  const void* ids;
+  int32_t id_bytes;
+  int32_t dtype;          /* of dout                                                    */
+  float scale;
+  const void* dout;
+  int64_t ldo;
+  float* dtable;
+  int64_t ldt;
+  int32_t accumulate;
+} dion_embed_grad;
+
+size_t dion_embed_backward_workspace(int64_t tokens, int64_t features);
+dion_status dion_embed_backward(const dion_embed_grad* args, void* d_workspace,
+                                size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

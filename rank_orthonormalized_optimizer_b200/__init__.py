@@ -461,3 +461,15 @@ def vec_step(x, g, m, v=None, *, rule="adamw", lr=None, betas=None, eps=None,
     (a one-off VecStepPlan; keep a plan for repeated steps).  Returns the launches."""
     return VecStepPlan(x, g, m, v, rule=rule, lr=lr, betas=betas, eps=eps,
                        weight_decay=weight_decay).step(step, stream)
+
+
+# ---------------------------------------------------------------- where gradients come from
+from . import gradients as _gradients  # noqa: E402
+from .gradients import (ACT_BLOCK, ActCheckpoint, EmbedGradPlan, EmbedPlan, NormGradPlan,  # noqa: E402,F401
+                        NormPlan, SavedStep, WeightGradPlan, dion_act_load, dion_act_save,
+                        dion_embed_backward, dion_embed_backward_workspace, dion_embed_lookup,
+                        dion_norm_backward, dion_norm_backward_workspace, dion_norm_forward,
+                        dion_step_batched_from_saved, dion_step_from_saved_workspace,
+                        dion_weight_grad, dion_weight_grad_workspace)
+
+EXPORTED += _gradients.EXPORTED

@@ -1224,6 +1224,53 @@ static dion_status dion_step_batched_from_host_impl(dion_handle h, const dion_bu
   return DION_OK;
 }
 
+// The sources of every matrix with G set to the matrix's slot, checked against the plan.
+static dion_status saved_sources(dion_handle h, const dion_bucket_ptrs* ptrs,
+                                 const dion_grad_source* sources,
+                                 std::vector<dion_grad_source>* out) {
+  if (!sources) return fail(DION_ERR_INVALID_ARG, "sources is NULL");
+  size_t i = 0;
+  for (size_t b = 0; b < h->plans.size(); ++b) {
+    const Plan& p = h->plans[b];
+    for (int32_t slot = 0; slot < p.count; ++slot, ++i) {
+      dion_grad_source s = sources[i];
+      const int64_t m = s.transposed ? s.n : s.kept.features;
+      const int64_t n = s.transposed ? s.kept.features : s.n;
+      if (m != p.m || n != p.n)
+        return fail(DION_ERR_INVALID_ARG, "source %zu gives a %lld x %lld gradient, the matrix is %lld x %lld",
+                    i, (long long)m, (long long)n, (long long)p.m, (long long)p.n);
+      s.G = ptrs ? const_cast<float*>(ptrs[b].G) + (size_t)slot * p.m * p.n : nullptr;
+      s.ldg = p.n;
+      out->push_back(s);
+    }
+  }
+  return DION_OK;
+}
+
+static dion_status dion_step_batched_from_saved_impl(dion_handle h, const dion_bucket_ptrs* ptrs,
+                                                     const dion_grad_source* sources,
+                                                     int32_t nbuckets, int32_t accumulate, float lr,
+                                                     void* d_workspace, size_t workspace_bytes,
+                                                     int32_t* d_status, int32_t* grad_status,
+                                                     void* stream) {
+  if (!valid(h)) return fail(DION_ERR_NOT_INITIALIZED, "invalid or freed handle");
+  if (h->sharded)
+    return fail(DION_ERR_INVALID_ARG, "a row-sharded plan steps through dion_step_sharded_begin");
+  if (!std::isfinite(lr)) return fail(DION_ERR_INVALID_ARG, "lr is not finite");
+  std::vector<dion_grad_source> list;
+  dion_status st = saved_sources(h, nullptr, sources, &list);  // the shapes
+  if (st == DION_OK) st = check_step_args(h, ptrs, nbuckets, d_workspace, workspace_bytes, d_status);
+  if (st != DION_OK) return st;
+  list.clear();
+  if ((st = saved_sources(h, ptrs, sources, &list)) != DION_OK) return st;
+  // every source is checked before the first gradient is enqueued; the workspace serves the
+  // gradients first and then the step, in the order of the stream
+  st = dion_weight_grad(list.data(), (int32_t)list.size(), accumulate, d_workspace, workspace_bytes,
+                        grad_status, stream);
+  if (st != DION_OK) return st;
+  return dion_step_batched_impl(h, ptrs, nbuckets, lr, d_workspace, workspace_bytes, d_status, stream);
+}
+
 // ------------------------------------------------------------ row-sharded step
 // Rank k holds rows [row0, row0 + m) of every matrix; Q is replicated.  The step runs
 // as the whole-matrix step, except that four quantities are summed over the ranks by
@@ -1640,6 +1687,29 @@ dion_status dion_step_batched_from_host(dion_handle h, const dion_bucket_ptrs* p
   return guarded("dion_step_batched_from_host", [&] {
     return dion_step_batched_from_host_impl(h, ptrs, host_grads, nbuckets, lr, d_workspace,
                                             workspace_bytes, d_status, host_status, stream);
+  });
+}
+
+size_t dion_step_from_saved_workspace(dion_handle h, const dion_grad_source* sources,
+                                      int32_t nsources) {
+  size_t bytes = 0;
+  guarded("dion_step_from_saved_workspace", [&] {
+    if (!valid(h)) return fail(DION_ERR_NOT_INITIALIZED, "invalid or freed handle");
+    bytes = dion_weight_grad_workspace(sources, nsources);
+    if (bytes < h->ws_bytes) bytes = h->ws_bytes;
+    return DION_OK;
+  });
+  return bytes;
+}
+
+dion_status dion_step_batched_from_saved(dion_handle h, const dion_bucket_ptrs* ptrs,
+                                         const dion_grad_source* sources, int32_t nbuckets,
+                                         int32_t accumulate, float lr, void* d_workspace,
+                                         size_t workspace_bytes, int32_t* d_status,
+                                         int32_t* grad_status, void* stream) {
+  return guarded("dion_step_batched_from_saved", [&] {
+    return dion_step_batched_from_saved_impl(h, ptrs, sources, nbuckets, accumulate, lr, d_workspace,
+                                             workspace_bytes, d_status, grad_status, stream);
   });
 }
 

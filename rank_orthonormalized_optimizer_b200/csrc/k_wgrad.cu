@@ -1,0 +1,610 @@
+// The gradient of a 2-D weight from activations kept in 8 bits:
+//
+//   G = A^T D   (m x n)      or, output-major,   G^T = D^T A   (n x m)
+//
+// A [tokens, m] are e4m3 bytes with a power-of-two scale per 32 features (rows.cuh), D
+// [tokens, n] bf16 gradients of the layer's output, G fp32: what the optimizer step reads.
+//
+// A's values are exact in bf16 and so are the products in fp32; the only roundings are the
+// fp32 additions.  The contraction over the tokens runs on the tensor cores: a persistent
+// CTA owns 128 x BN tiles of G and walks the tokens 64 at a time,
+//   warp 0        TMA producer: the 8-bit tile (64 tokens x 128 features) and the D tile
+//   warp 1        MMA issuer (one thread)
+//   warp 2        TMEM allocator
+//   warps 4..7    converters: e4m3 and scale -> bf16, written as the 128-byte-swizzled
+//                 MN-major operand that tcgen05.mma reads
+//   warps 8..15   epilogue
+// The tensor cores' accumulation rounds toward zero, which adds up over thousands of MMAs,
+// so the tokens are cut into chunks of kChunk blocks, each accumulated from zero in TMEM
+// (two accumulators in turn), and the epilogue warps add the chunks in fp32 registers.
+// Where the tiles are fewer than the SMs the tokens are also split over CTAs; the partial
+// sums go to the workspace and a second kernel adds them in order.  Every wait is bounded.
+#include <cuda.h>
+
+#include <cstdio>
+
+#include "common.cuh"
+#include "operator.h"
+#include "rows.cuh"
+#include "tc_ptx.cuh"
+
+namespace dion {
+namespace {
+
+using namespace tc;
+
+constexpr int BM = 128;      // features of A per tile = TMEM lanes
+constexpr int BK = 64;       // tokens per stage
+constexpr int kChunk = 4;    // stages per accumulation chunk
+constexpr int NT = 512;
+constexpr int SQ = 4;        // stages of the 8-bit tiles and of D
+constexpr int SA = 3;        // stages of the converted operand
+constexpr int Q_BYTES = BK * BM;
+constexpr int A_BYTES = BK * BM * 2;
+constexpr int64_t kMaxSpins = int64_t(1) << 26;
+
+struct WgradP {
+  const uint8_t* scale;
+  float* out;        // G, or the partial sums [splits][m][n] (row-major always)
+  int32_t* status;
+  int64_t tokens, ld_scale, ldg, m, n;
+  int tiles_m, tiles_n, splits, blocks_per_split, blocks;  // blocks: of 64 tokens
+  int transposed, accumulate, vec;
+  int64_t max_spins;
+};
+
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, uint64_t* bar, int c0,
+                                            int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      : "memory");
+}
+template <int R> __device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R> __device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+// Two e4m3 bytes of `w` (the pair chosen by `sel`) to bf16 times `f`.  The 7 magnitude
+// bits, moved to bf16's exponent and fraction, read as the value times 2^-120 (subnormals
+// too: both formats count them in steps of their smallest normal); the two factors 2^120
+// and f are powers of two, so both products are exact.
+__device__ __forceinline__ uint32_t e4m3x2_bf16(uint32_t w, uint32_t sel, uint32_t f) {
+  const uint32_t p = __byte_perm(w, 0, sel);  // the bytes in the high halves: sign at bit 15
+  const uint32_t b = (p & 0x80008000u) | ((p >> 4) & 0x07f007f0u);
+  uint32_t r;
+  asm("{\n\t.reg .b32 t;\n\tmul.rn.bf16x2 t, %1, %2;\n\tmul.rn.bf16x2 %0, t, %3;\n\t}"
+      : "=r"(r) : "r"(b), "r"(0x7b807b80u), "r"(f));
+  return r;
+}
+
+// A unit of work: one tile over one range of token blocks.
+struct Unit {
+  int m0, n0, split, kb0, kb1;
+};
+template <int BN>
+__device__ __forceinline__ Unit unit_of(const WgradP& p, int u) {
+  Unit t;
+  const int tiles = p.tiles_m * p.tiles_n;
+  t.split = u / tiles;
+  const int rem = u - t.split * tiles;
+  t.m0 = (rem % p.tiles_m) * BM;
+  t.n0 = (rem / p.tiles_m) * BN;
+  t.kb0 = t.split * p.blocks_per_split;
+  t.kb1 = min(p.blocks, t.kb0 + p.blocks_per_split);
+  return t;
+}
+
+template <int BN>
+__global__ void __launch_bounds__(NT, 1)
+    k_wgrad(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmD,
+            const WgradP p) {
+  constexpr int B_BYTES = BK * BN * 2;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  uint8_t* sA = smem;
+  uint8_t* sB = sA + SA * A_BYTES;
+  uint8_t* sQ = sB + SQ * B_BYTES;
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(sQ + SQ * Q_BYTES);
+  uint64_t* q_empty = q_full + SQ;
+  uint64_t* b_full = q_empty + SQ;
+  uint64_t* b_empty = b_full + SQ;
+  uint64_t* a_full = b_empty + SQ;
+  uint64_t* a_empty = a_full + SA;
+  uint64_t* tfull = a_empty + SA;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int units = p.tiles_m * p.tiles_n * p.splits;
+  constexpr uint32_t kCols = 2 * BN;  // TMEM columns: two accumulators
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < SQ; ++s) {
+      mbar_init(q_full + s, 1);
+      mbar_init(q_empty + s, 4);
+      mbar_init(b_full + s, 1);
+      mbar_init(b_empty + s, 1);
+    }
+    for (int s = 0; s < SA; ++s) {
+      mbar_init(a_full + s, 4);
+      mbar_init(a_empty + s, 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull + a, 1);
+      mbar_init(tempty + a, 8);
+    }
+    mbar_init(drain, 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) {
+    tmem_alloc(tmem_slot, kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp < 4) {
+    reg_dec<56>();
+    if (warp == 0 && lane == 0) {
+      // ---------------- TMA producer
+      prefetch_map(&tmQ);
+      prefetch_map(&tmD);
+      int stage = 0, used = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+        const Unit t = unit_of<BN>(p, u);
+        for (int kb = t.kb0; kb < t.kb1; ++kb) {
+          if (!wait_bounded(q_empty + stage, phase ^ 1, p.max_spins, abort) ||
+              !wait_bounded(b_empty + stage, phase ^ 1, p.max_spins, abort)) { ok = false; break; }
+          mbar_expect_tx(q_full + stage, Q_BYTES);
+          tma_load_2d(sQ + stage * Q_BYTES, &tmQ, q_full + stage, t.m0, kb * BK);
+          mbar_expect_tx(b_full + stage, B_BYTES);
+#pragma unroll
+          for (int j = 0; j < BN / 64; ++j)
+            tma_load_2d(sB + stage * B_BYTES + j * 8192, &tmD, b_full + stage, t.n0 + 64 * j, kb * BK);
+          if (used < SQ) ++used;
+          if (++stage == SQ) { stage = 0; phase ^= 1; }
+        }
+      }
+      if (*abort)  // let every load already issued land before the CTA goes away
+        for (int i = 0; i < used; ++i) {
+          stage = (stage + SQ - 1) % SQ;
+          if (stage == SQ - 1) phase ^= 1;
+          wait_drain(q_full + stage, phase);
+          wait_drain(b_full + stage, phase);
+        }
+    } else if (warp == 1 && lane == 0) {
+      // ---------------- MMA issuer
+      constexpr uint32_t idesc = idesc_bf16(BM, BN, true, true);
+      int sb = 0, sa = 0, acc = 0;
+      uint32_t pb = 0, pa = 0, pacc = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+        const Unit t = unit_of<BN>(p, u);
+        for (int c0 = t.kb0; c0 < t.kb1 && ok; c0 += kChunk) {
+          if (!wait_bounded(tempty + acc, pacc ^ 1, p.max_spins, abort)) { ok = false; break; }
+          tc_fence_after();
+          const int c1 = min(t.kb1, c0 + kChunk);
+          for (int kb = c0; kb < c1; ++kb) {
+            if (!wait_bounded(b_full + sb, pb, p.max_spins, abort) ||
+                !wait_bounded(a_full + sa, pa, p.max_spins, abort)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t ab = smem_u32(sA + sa * A_BYTES), bb = smem_u32(sB + sb * B_BYTES);
+#pragma unroll
+            for (int k = 0; k < BK / 16; ++k)
+              mma_bf16(tmem + acc * BN, sw128_desc(ab + k * 2048, 8192, 1024),
+                       sw128_desc(bb + k * 2048, 8192, 1024), idesc, ((kb - c0) | k) != 0);
+            mma_commit(b_empty + sb);
+            mma_commit(a_empty + sa);
+            if (++sb == SQ) { sb = 0; pb ^= 1; }
+            if (++sa == SA) { sa = 0; pa ^= 1; }
+          }
+          if (!ok) break;
+          mma_commit(tfull + acc);
+          acc ^= 1;
+          if (acc == 0) pacc ^= 1;
+        }
+      }
+      mma_commit(drain);
+      wait_drain(drain, 0);
+    }
+  } else if (warp < 8) {
+    // ---------------- converters: 16 features of a token at a time
+    reg_dec<112>();
+    const int tid = threadIdx.x - 128;
+    const int c = tid & 7;                      // features 16 c .. 16 c + 15 of the tile
+    const int swap = c >= 4 ? 1 : 0;            // halves store in opposite order: no bank conflict
+    int sq = 0, sa = 0;
+    uint32_t pq = 0, pa = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      const Unit t = unit_of<BN>(p, u);
+      const int64_t sc = (t.m0 + 16 * c) / 32;
+      const uint8_t* scale = p.scale + sc;
+      const bool in = sc < p.ld_scale;
+      uint32_t E[4];
+      auto scales = [&](int kb) {  // of this thread's four tokens (0: past the end)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int64_t tok = (int64_t)kb * BK + (tid >> 3) + 16 * i;
+          E[i] = in && kb < t.kb1 && tok < p.tokens ? scale[tok * p.ld_scale] : 0u;
+        }
+      };
+      scales(t.kb0);
+      for (int kb = t.kb0; kb < t.kb1; ++kb) {
+        const bool w = wait_bounded(q_full + sq, pq, p.max_spins, abort) &&
+                       wait_bounded(a_empty + sa, pa ^ 1, p.max_spins, abort);
+        if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+        const uint8_t* src = sQ + sq * Q_BYTES;
+        uint8_t* dst = sA + sa * A_BYTES + (c >> 2) * 8192;
+        uint4 raw[4];
+        uint32_t f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          raw[i] = *reinterpret_cast<const uint4*>(src + ((tid >> 3) + 16 * i) * BM + c * 16);
+          // 2^(E - 127) as bf16; a marked block is NaN; tokens past the end are zeros
+          const uint32_t h = E[i] == 255u ? 0x7fc0u : E[i] << 7;
+          f[i] = h | h << 16;
+        }
+        scales(kb + 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int k = (tid >> 3) + 16 * i;
+          uint4 lo, hi;
+          lo.x = e4m3x2_bf16(raw[i].x, 0x1404, f[i]);
+          lo.y = e4m3x2_bf16(raw[i].x, 0x3424, f[i]);
+          lo.z = e4m3x2_bf16(raw[i].y, 0x1404, f[i]);
+          lo.w = e4m3x2_bf16(raw[i].y, 0x3424, f[i]);
+          hi.x = e4m3x2_bf16(raw[i].z, 0x1404, f[i]);
+          hi.y = e4m3x2_bf16(raw[i].z, 0x3424, f[i]);
+          hi.z = e4m3x2_bf16(raw[i].w, 0x1404, f[i]);
+          hi.w = e4m3x2_bf16(raw[i].w, 0x3424, f[i]);
+          const int j = 2 * (c & 3);
+          const uint4 first = swap ? hi : lo, second = swap ? lo : hi;
+          *reinterpret_cast<uint4*>(dst + k * 128 + (((j + swap) ^ (k & 7)) << 4)) = first;
+          *reinterpret_cast<uint4*>(dst + k * 128 + (((j + 1 - swap) ^ (k & 7)) << 4)) = second;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(q_empty + sq);
+          mbar_arrive(a_full + sa);
+        }
+        if (++sq == SQ) { sq = 0; pq ^= 1; }
+        if (++sa == SA) { sa = 0; pa ^= 1; }
+      }
+    }
+  } else {
+    // ---------------- epilogue: a warp owns 32 features and half of the tile's columns
+    reg_inc<168>();
+    const int ew = warp - 8;
+    const int row0 = (ew & 3) * 32;
+    constexpr int HB = BN / 2;
+    const int col0 = (ew >> 2) * HB;
+    int acc = 0;
+    uint32_t pacc = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      const Unit t = unit_of<BN>(p, u);
+      float run[HB];
+#pragma unroll
+      for (int i = 0; i < HB; ++i) run[i] = 0.f;
+      for (int c0 = t.kb0; c0 < t.kb1; c0 += kChunk) {
+        const bool w = wait_bounded(tfull + acc, pacc, p.max_spins, abort);
+        if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t base = tmem + ((uint32_t)row0 << 16) + acc * BN + col0;
+#pragma unroll
+        for (int c = 0; c < HB; c += 16) {
+          float v[16];
+          tmem_ld16(base + c, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) run[c + i] += v[i];
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tempty + acc);
+        acc ^= 1;
+        if (acc == 0) pacc ^= 1;
+      }
+      if (!ok) break;
+      const int64_t row = t.m0 + row0 + lane;
+      const int64_t n0 = t.n0 + col0;
+      if (row >= p.m) {
+        // a lane past the last feature writes nothing
+      } else if (p.transposed && p.splits == 1) {
+        // 32 lanes write 32 neighbouring features of one column
+#pragma unroll
+        for (int i = 0; i < HB; ++i)
+          if (n0 + i < p.n) {
+            float* g = p.out + (n0 + i) * p.ldg + row;
+            *g = run[i] + (p.accumulate ? *g : 0.f);
+          }
+      } else {
+        const bool part = p.splits > 1;
+        float* g = part ? p.out + ((int64_t)t.split * p.m + row) * p.n + n0 : p.out + row * p.ldg + n0;
+        const bool add = p.accumulate && !part;
+#pragma unroll
+        for (int i = 0; i < HB; i += 4) {
+          if (p.vec && n0 + i + 3 < p.n) {
+            float4 o = make_float4(run[i], run[i + 1], run[i + 2], run[i + 3]);
+            if (add) {
+              const float4 a = *reinterpret_cast<const float4*>(g + i);
+              o.x += a.x; o.y += a.y; o.z += a.z; o.w += a.w;
+            }
+            *reinterpret_cast<float4*>(g + i) = o;
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (n0 + i + j < p.n) g[i + j] = run[i + j] + (add ? g[i + j] : 0.f);
+          }
+        }
+      }
+      __syncwarp();  // the next unit's TMEM loads are warp-wide
+    }
+    if ((!ok || *abort) && lane == 0 && p.status) atomicOr(p.status, F_TIMEOUT);
+  }
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kCols);
+  }
+}
+
+// Adds the splits' partial sums in order, into G in either layout.
+__global__ void __launch_bounds__(256) k_wgrad_join(const float* parts, float* G, int64_t ldg,
+                                                    int64_t m, int64_t n, int splits, int transposed,
+                                                    int accumulate) {
+  __shared__ float tile[32][33];
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int64_t i0 = (int64_t)blockIdx.y * 32, j0 = (int64_t)blockIdx.x * 32;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int64_t i = i0 + ty + 8 * k, j = j0 + tx;
+    float a = 0.f;
+    if (i < m && j < n) {
+#pragma unroll 4
+      for (int s = 0; s < splits; ++s) a += parts[((int64_t)s * m + i) * n + j];
+      if (!transposed) {
+        float* g = G + i * ldg + j;
+        *g = a + (accumulate ? *g : 0.f);
+      }
+    }
+    tile[ty + 8 * k][tx] = a;
+  }
+  if (!transposed) return;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int64_t j = j0 + ty + 8 * k, i = i0 + tx;
+    if (i < m && j < n) {
+      float* g = G + j * ldg + i;
+      *g = tile[tx][ty + 8 * k] + (accumulate ? *g : 0.f);
+    }
+  }
+}
+
+// D into rows that a TMA map can take (a multiple of 8 columns, the rest zero).
+__global__ void __launch_bounds__(256) k_wgrad_pad(const __nv_bfloat16* d, int64_t ldd,
+                                                   __nv_bfloat16* out, int64_t ldo, int64_t tokens,
+                                                   int64_t n) {
+  const int64_t total = tokens * ldo;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / ldo, col = i - row * ldo;
+    out[i] = col < n ? d[row * ldd + col] : __float2bfloat16_rn(0.f);
+  }
+}
+
+__global__ void __launch_bounds__(256) k_wgrad_zero(float* G, int64_t ldg, int64_t rows, int64_t cols) {
+  const int64_t total = rows * cols;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / cols;
+    G[row * ldg + i - row * cols] = 0.f;
+  }
+}
+
+// ---------------------------------------------------------------- host
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static const EncodeTiledFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiledFn>(p);
+  }();
+  return fn;
+}
+
+// 2-D map of [rows][cols] with rows `stride` bytes apart, box {b0, b1}.
+dion_status map2d(CUtensorMap* m, const void* base, CUtensorMapDataType type,
+                  CUtensorMapSwizzle swizzle, uint64_t cols, uint64_t rows, uint64_t stride,
+                  uint32_t b0, uint32_t b1) {
+  const EncodeTiledFn f = encode_fn();
+  if (!f) return set_error(DION_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {stride};
+  cuuint32_t box[2] = {b0, b1};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r = f(m, type, 2, const_cast<void*>(base), dims, strides, box, estr,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return set_error(DION_ERR_CUDA, "cuTensorMapEncodeTiled -> %d (%llu x %llu, stride %llu)", (int)r,
+                     (unsigned long long)rows, (unsigned long long)cols, (unsigned long long)stride);
+  return DION_OK;
+}
+
+#define DION_TRY(call)              \
+  do {                              \
+    const dion_status st_ = (call); \
+    if (st_ != DION_OK) return st_; \
+  } while (0)
+
+constexpr int kSms = 148;  // plans (and so workspace sizes) do not depend on the device asked
+
+struct GradPlan {
+  int bn, tiles_m, tiles_n, splits, blocks, blocks_per_split;
+  bool pad;
+  int64_t ldd;          // of the padded copy
+  size_t parts_bytes, pad_bytes;
+};
+
+size_t up256(size_t b) { return (b + 255) / 256 * 256; }
+
+GradPlan plan_of(const dion_grad_source& s) {
+  GradPlan g{};
+  const int64_t m = s.kept.features, n = s.n;
+  g.bn = n > 128 ? 256 : n > 64 ? 128 : 64;
+  g.tiles_m = (int)((m + BM - 1) / BM);
+  g.tiles_n = (int)((n + g.bn - 1) / g.bn);
+  g.blocks = (int)((s.kept.tokens + BK - 1) / BK);
+  // tokens are split where a second tile's worth of SMs would idle, whole chunks each
+  const int64_t tiles = (int64_t)g.tiles_m * g.tiles_n;
+  const int chunks = (g.blocks + kChunk - 1) / kChunk;
+  int64_t want = tiles > 0 ? kSms / tiles : 1;
+  if (want > chunks) want = chunks;
+  if (want < 1) want = 1;
+  const int per = chunks > 0 ? (int)((chunks + want - 1) / want) : 1;
+  g.blocks_per_split = per * kChunk;
+  g.splits = chunks > 0 ? (chunks + per - 1) / per : 1;
+  g.pad = !rows_aligned16(s.d, s.ldd, 2);
+  g.ldd = (n + 7) / 8 * 8;
+  g.parts_bytes = g.splits > 1 ? up256((size_t)g.splits * m * n * 4) : 0;
+  g.pad_bytes = g.pad ? up256((size_t)s.kept.tokens * g.ldd * 2) : 0;
+  return g;
+}
+
+dion_status check_source(const dion_grad_source& s, int i) {
+  DION_TRY(check_kept(s.kept));
+  if (s.kept.features > (1 << 24) || s.n < 1 || s.n > (1 << 24))
+    return set_error(DION_ERR_UNSUPPORTED_SHAPE, "source %d: m and n must lie in [1, 2^24]", i);
+  if (s.kept.tokens > INT32_MAX - BK * kChunk)
+    return set_error(DION_ERR_UNSUPPORTED_SHAPE, "source %d: too many tokens", i);
+  if (s.kept.tokens > 0) DION_TRY(check_rows("d", s.d, s.ldd, s.n, 2));
+  DION_TRY(check_rows("G", s.G, s.ldg, s.transposed ? s.kept.features : s.n, 4));
+  return DION_OK;
+}
+
+template <int BN>
+dion_status launch(const CUtensorMap& mq, const CUtensorMap& md, const WgradP& p, int sms, cudaStream_t s) {
+  constexpr size_t smem = 1024 + SA * A_BYTES + SQ * (BK * BN * 2 + Q_BYTES) +
+                          (4 * SQ + 2 * SA + 5) * 8 + 16;
+  const cudaError_t e = cudaFuncSetAttribute(k_wgrad<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)smem);
+  if (e != cudaSuccess) return set_error(DION_ERR_CUDA, "k_wgrad: %s", cudaGetErrorString(e));
+  const int64_t units = (int64_t)p.tiles_m * p.tiles_n * p.splits;
+  k_wgrad<BN><<<(unsigned)(units < sms ? units : sms), NT, smem, s>>>(mq, md, p);
+  return launch_status("k_wgrad");
+}
+
+dion_status one_grad(const dion_grad_source& src, int accumulate, char* ws, int32_t* status, int sms,
+                     cudaStream_t s) {
+  const int64_t m = src.kept.features, n = src.n, tokens = src.kept.tokens;
+  if (tokens == 0) {
+    if (accumulate) return DION_OK;
+    k_wgrad_zero<<<sms * 4, 256, 0, s>>>(src.G, src.ldg, src.transposed ? n : m, src.transposed ? m : n);
+    return launch_status("k_wgrad_zero");
+  }
+  const GradPlan g = plan_of(src);
+  const void* d = src.d;
+  int64_t ldd = src.ldd;
+  if (g.pad) {
+    __nv_bfloat16* copy = reinterpret_cast<__nv_bfloat16*>(ws + g.parts_bytes);
+    k_wgrad_pad<<<sms * 8, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(src.d), src.ldd, copy, g.ldd,
+                                        tokens, n);
+    DION_TRY(launch_status("k_wgrad_pad"));
+    d = copy;
+    ldd = g.ldd;
+  }
+  const int64_t ld = kept_ld(m);
+  CUtensorMap mq, md;
+  DION_TRY(map2d(&mq, src.kept.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE,
+                 (uint64_t)ld, (uint64_t)tokens, (uint64_t)ld, BM, BK));
+  DION_TRY(map2d(&md, d, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, (uint64_t)n,
+                 (uint64_t)tokens, (uint64_t)ldd * 2, 64, BK));
+  WgradP p{};
+  p.scale = src.kept.scale;
+  p.out = g.splits > 1 ? reinterpret_cast<float*>(ws) : src.G;
+  p.status = status;
+  p.tokens = tokens;
+  p.ld_scale = ld / DION_ACT_BLOCK;
+  p.ldg = src.ldg;
+  p.m = m;
+  p.n = n;
+  p.tiles_m = g.tiles_m;
+  p.tiles_n = g.tiles_n;
+  p.splits = g.splits;
+  p.blocks = g.blocks;
+  p.blocks_per_split = g.blocks_per_split;
+  p.transposed = src.transposed != 0;
+  p.accumulate = accumulate != 0;
+  p.vec = g.splits > 1 ? n % 4 == 0 : rows_aligned16(src.G, src.ldg, 4);
+  p.max_spins = kMaxSpins;
+  dion_status st = g.bn == 256 ? launch<256>(mq, md, p, sms, s)
+                   : g.bn == 128 ? launch<128>(mq, md, p, sms, s) : launch<64>(mq, md, p, sms, s);
+  if (st != DION_OK || g.splits == 1) return st;
+  k_wgrad_join<<<dim3((unsigned)((n + 31) / 32), (unsigned)((m + 31) / 32)), 256, 0, s>>>(
+      reinterpret_cast<const float*>(ws), src.G, src.ldg, m, n, g.splits, p.transposed, p.accumulate);
+  return launch_status("k_wgrad_join");
+}
+
+dion_status wgrad_impl(const dion_grad_source* src, int32_t nsrc, int32_t accumulate, void* ws,
+                       size_t ws_bytes, int32_t* d_status, void* stream) {
+  if (nsrc < 0) return set_error(DION_ERR_INVALID_ARG, "nsources < 0");
+  if (nsrc > 0 && !src) return set_error(DION_ERR_INVALID_ARG, "sources is NULL");
+  for (int32_t i = 0; i < nsrc; ++i) DION_TRY(check_source(src[i], i));
+  const size_t need = dion_weight_grad_workspace(src, nsrc);
+  if (need && !ws) return set_error(DION_ERR_INVALID_ARG, "workspace is NULL");
+  if (ws_bytes < need)
+    return set_error(DION_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes, %zu needed", ws_bytes, need);
+  if (!aligned_to(ws, 16)) return set_error(DION_ERR_MISALIGNED, "workspace is not 16-byte aligned");
+  if (d_status && !aligned_to(d_status, 4))
+    return set_error(DION_ERR_MISALIGNED, "d_status is not 4-byte aligned");
+  int sms = 0;
+  DION_TRY(check_sm100(&sms));
+  for (int32_t i = 0; i < nsrc; ++i)
+    DION_TRY(one_grad(src[i], accumulate, static_cast<char*>(ws), d_status ? d_status + i : nullptr, sms,
+                      reinterpret_cast<cudaStream_t>(stream)));
+  return DION_OK;
+}
+
+}  // namespace
+}  // namespace dion
+
+extern "C" {
+
+size_t dion_weight_grad_workspace(const dion_grad_source* sources, int32_t nsources) {
+  size_t most = 0;
+  for (int32_t i = 0; sources && i < nsources; ++i) {
+    if (dion::check_source(sources[i], i) != DION_OK) return 0;
+    const dion::GradPlan g = dion::plan_of(sources[i]);
+    const size_t b = g.parts_bytes + g.pad_bytes;
+    most = b > most ? b : most;
+  }
+  return most;
+}
+
+dion_status dion_weight_grad(const dion_grad_source* sources, int32_t nsources, int32_t accumulate,
+                             void* d_workspace, size_t workspace_bytes, int32_t* d_status,
+                             void* stream) {
+  return dion::wgrad_impl(sources, nsources, accumulate, d_workspace, workspace_bytes, d_status, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,87 @@
+// Host-side checks shared by the operators that give the step its gradients
+// (k_act.cu, k_norm.cu, k_embed.cu, k_wgrad.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <cmath>
+
+#include "internal.h"
+
+namespace dion {
+
+// The current device must be an sm_100; *sms receives its SM count.
+inline dion_status check_sm100(int* sms) {
+  int dev = -1;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return set_error(DION_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
+  int major = 0, minor = 0;
+  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+  if (major != 10 || minor != 0)
+    return set_error(DION_ERR_DEVICE,
+                     "device %d is sm_%d%d; this library is built for sm_100a (B200)", dev, major,
+                     minor);
+  *sms = 0;
+  cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (*sms <= 0) *sms = 148;
+  return DION_OK;
+}
+
+inline dion_status launch_status(const char* what) {
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? DION_OK
+                          : set_error(DION_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+inline bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+inline bool valid_dtype(int32_t t) { return t == DION_BF16 || t == DION_FP16 || t == DION_FP32; }
+inline int64_t dtype_bytes(int32_t t) { return t == DION_FP32 ? 4 : 2; }
+
+// Largest sizes taken: a grid's x dimension holds a row of each, and every offset
+// tokens * ld stays far below 2^63.
+constexpr int64_t kMaxTokens = INT32_MAX;
+constexpr int64_t kMaxLd = int64_t(1) << 31;
+
+inline dion_status check_tokens(int64_t tokens) {
+  if (tokens < 0 || tokens > kMaxTokens)
+    return set_error(DION_ERR_INVALID_ARG, "tokens %lld outside [0, 2^31)", (long long)tokens);
+  return DION_OK;
+}
+
+// A row-major [tokens, features] array with rows ld elements apart.
+inline dion_status check_rows(const char* name, const void* p, int64_t ld, int64_t features,
+                              int64_t elem) {
+  if (!p) return set_error(DION_ERR_INVALID_ARG, "%s is NULL", name);
+  if (ld < features || ld > kMaxLd)
+    return set_error(DION_ERR_INVALID_ARG, "%s: row stride %lld outside [features %lld, 2^31]", name,
+                     (long long)ld, (long long)features);
+  if (!aligned_to(p, (size_t)elem))
+    return set_error(DION_ERR_MISALIGNED, "%s is not aligned to its %d-byte elements", name,
+                     (int)elem);
+  return DION_OK;
+}
+
+// Whether every row of the array starts on a 16-byte boundary.
+inline bool rows_aligned16(const void* p, int64_t ld, int64_t elem) {
+  return aligned_to(p, 16) && (ld * elem) % 16 == 0;
+}
+
+// Rows of the 8-bit form: features rounded up to whole blocks.
+inline int64_t kept_ld(int64_t features) { return (features + DION_ACT_BLOCK - 1) / DION_ACT_BLOCK * DION_ACT_BLOCK; }
+
+inline dion_status check_kept(const dion_act_kept& k) {
+  dion_status st = check_tokens(k.tokens);
+  if (st != DION_OK) return st;
+  if (k.features < 1 || k.features > kMaxLd - DION_ACT_BLOCK)
+    return set_error(DION_ERR_INVALID_ARG, "features %lld outside [1, 2^31 - 32]", (long long)k.features);
+  if (k.tokens == 0) return DION_OK;
+  if (!k.q || !k.scale) return set_error(DION_ERR_INVALID_ARG, "the 8-bit rows: a NULL pointer");
+  if (!aligned_to(k.q, 16))
+    return set_error(DION_ERR_MISALIGNED, "the 8-bit rows are not 16-byte aligned");
+  return DION_OK;
+}
+
+}  // namespace dion
