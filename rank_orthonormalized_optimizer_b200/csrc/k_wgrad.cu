@@ -6,18 +6,21 @@
 // [tokens, n] bf16 gradients of the layer's output, G fp32: what the optimizer step reads.
 //
 // A's values are exact in bf16 and so are the products in fp32; the only roundings are the
-// fp32 additions.  The contraction over the tokens runs on the tensor cores: a persistent
-// CTA owns 128 x BN tiles of G and walks the tokens 64 at a time,
-//   warp 0        TMA producer: the 8-bit tile (64 tokens x 128 features) and the D tile
-//   warp 1        MMA issuer (one thread)
+// fp32 additions.  The contraction over the tokens runs on the tensor cores: a persistent pair
+// of CTAs (a cluster, tcgen05 cta_group::2) owns 256 x BN tiles of G, each CTA 128 of the
+// features and half of the columns, and walks the tokens 64 at a time.  In each CTA
+//   warp 0        TMA producer: the 8-bit tile (64 tokens x 128 features), half of the D tile
+//   warp 1        MMA issuer (one thread, in the pair's first CTA)
 //   warp 2        TMEM allocator
-//   warps 4..7    converters: e4m3 and scale -> bf16, written as the 128-byte-swizzled
-//                 MN-major operand that tcgen05.mma reads
-//   warps 8..15   epilogue
+//   warp 3        the tile's scale bytes (cp.async)
+//   warps 4..11   converters: e4m3 and scale -> bf16, written as the 128-byte-swizzled
+//                 MN-major operand that tcgen05.mma reads; two groups of four take every
+//                 other stage, so that one group's latencies pass behind the other's work
+//   warps 12..19  epilogue
 // The tensor cores' accumulation rounds toward zero, which adds up over thousands of MMAs,
 // so the tokens are cut into chunks of kChunk blocks, each accumulated from zero in TMEM
 // (two accumulators in turn), and the epilogue warps add the chunks in fp32 registers.
-// Where the tiles are fewer than the SMs the tokens are also split over CTAs; the partial
+// Where the tiles are fewer than the pairs the tokens are also split over pairs; the partial
 // sums go to the workspace and a second kernel adds them in order.  Every wait is bounded.
 #include <cuda.h>
 
@@ -33,12 +36,15 @@ namespace {
 
 using namespace tc;
 
-constexpr int BM = 128;      // features of A per tile = TMEM lanes
+constexpr int BM = 128;      // features of A per CTA = TMEM lanes
+constexpr int PM = 2 * BM;   // features of a pair's tile
 constexpr int BK = 64;       // tokens per stage
-constexpr int kChunk = 4;    // stages per accumulation chunk
-constexpr int NT = 512;
-constexpr int SQ = 4;        // stages of the 8-bit tiles and of D
-constexpr int SA = 3;        // stages of the converted operand
+constexpr int kChunk = 8;    // stages per accumulation chunk
+constexpr int NT = 640;
+constexpr int SQ = 6;        // stages of the 8-bit and D tiles
+constexpr int SA = 4;        // stages of the converted operand
+constexpr int kGroups = 2, kGroupWarps = 4;                // converters
+constexpr int kItems = BK * BM / 16 / (32 * kGroupWarps);  // 16-feature groups per thread
 constexpr int Q_BYTES = BK * BM;
 constexpr int A_BYTES = BK * BM * 2;
 constexpr int64_t kMaxSpins = int64_t(1) << 26;
@@ -50,6 +56,7 @@ struct WgradP {
   int64_t tokens, ld_scale, ldg, m, n;
   int tiles_m, tiles_n, splits, blocks_per_split, blocks;  // blocks: of 64 tokens
   int transposed, accumulate, vec;
+  int scale4;        // the scale bytes of a tile's token are an aligned word
   int64_t max_spins;
 };
 
@@ -61,6 +68,15 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, uin
       "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                 "=r"(r[7])
+               : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
 template <int R> __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
 }
@@ -68,17 +84,70 @@ template <int R> __device__ __forceinline__ void reg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
-// Two e4m3 bytes of `w` (the pair chosen by `sel`) to bf16 times `f`.  The 7 magnitude
-// bits, moved to bf16's exponent and fraction, read as the value times 2^-120 (subnormals
-// too: both formats count them in steps of their smallest normal); the two factors 2^120
-// and f are powers of two, so both products are exact.
-__device__ __forceinline__ uint32_t e4m3x2_bf16(uint32_t w, uint32_t sel, uint32_t f) {
-  const uint32_t p = __byte_perm(w, 0, sel);  // the bytes in the high halves: sign at bit 15
-  const uint32_t b = (p & 0x80008000u) | ((p >> 4) & 0x07f007f0u);
+// ---- the pair: barriers of the first CTA, MMAs and TMEM of both
+__device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
-  asm("{\n\t.reg .b32 t;\n\tmul.rn.bf16x2 t, %1, %2;\n\tmul.rn.bf16x2 %0, t, %3;\n\t}"
-      : "=r"(r) : "r"(b), "r"(0x7b807b80u), "r"(f));
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the same barrier in the pair's first CTA
+__device__ __forceinline__ uint32_t first_cta(uint64_t* bar) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(bar)));
+  return r;
+}
+// What an arrival hands over lies in the arriver's own shared memory (ordered before it by the
+// proxy fence) or in TMEM (by the tcgen05 fences), so the CTA-scope default is enough; with
+// cluster-scope release and acquire each arrival waited about 1600 cycles for every earlier
+// memory operation of its thread, and the kernel ran at 690 TFLOP/s.
+__device__ __forceinline__ void arrive_remote(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                         uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+// Arrive on `bar` of both CTAs once the MMAs issued so far have completed.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* slot, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)),
+               "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+// Four e4m3 bytes to bf16 times `f`: bytes 0 and 2 to `even`, 1 and 3 to `odd`.  A byte's 7
+// magnitude bits, moved to bf16's exponent and fraction, read as its value times 2^-120
+// (subnormals too: both formats count them in steps of their smallest normal).  f carries the
+// 2^120; all products are exact, being by powers of two.  Taking every other byte needs no
+// byte permutation; the features' order in the tile is then 0 2 1 3 of each four, which the
+// epilogue undoes.
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void e4m3x4_bf16(uint32_t w, uint32_t f, uint32_t& even, uint32_t& odd) {
+  constexpr uint32_t M = 0x07f007f0u;   // the magnitude's place
+  const uint32_t s = w & 0x80808080u;   // signs; the other pair's fall inside M, and out
+  even = bf16x2_mul(((w << 4) & M) | ((s << 8) & ~M), f);
+  odd = bf16x2_mul(((w >> 4) & M) | (s & ~M), f);
 }
 
 // A unit of work: one tile over one range of token blocks.
@@ -91,7 +160,7 @@ __device__ __forceinline__ Unit unit_of(const WgradP& p, int u) {
   const int tiles = p.tiles_m * p.tiles_n;
   t.split = u / tiles;
   const int rem = u - t.split * tiles;
-  t.m0 = (rem % p.tiles_m) * BM;
+  t.m0 = (rem % p.tiles_m) * PM;
   t.n0 = (rem / p.tiles_m) * BN;
   t.kb0 = t.split * p.blocks_per_split;
   t.kb1 = min(p.blocks, t.kb0 + p.blocks_per_split);
@@ -99,61 +168,61 @@ __device__ __forceinline__ Unit unit_of(const WgradP& p, int u) {
 }
 
 template <int BN>
-__global__ void __launch_bounds__(NT, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
     k_wgrad(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmD,
             const WgradP p) {
-  constexpr int B_BYTES = BK * BN * 2;
+  constexpr int HB = BN / 2;               // columns of D that a CTA loads
+  constexpr int B_BYTES = BK * HB * 2;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = align1024(smem_raw);
+  uint8_t* smem = align1024(smem_raw);     // the same offset in both CTAs
   uint8_t* sA = smem;
   uint8_t* sB = sA + SA * A_BYTES;
   uint8_t* sQ = sB + SQ * B_BYTES;
-  uint64_t* q_full = reinterpret_cast<uint64_t*>(sQ + SQ * Q_BYTES);
-  uint64_t* q_empty = q_full + SQ;
-  uint64_t* b_full = q_empty + SQ;
-  uint64_t* b_empty = b_full + SQ;
-  uint64_t* a_full = b_empty + SQ;
+  uint32_t* sS = reinterpret_cast<uint32_t*>(sQ + SQ * Q_BYTES);  // [stage][token]: 4 scale bytes
+  uint64_t* full = reinterpret_cast<uint64_t*>(sS + SQ * BK);     // both tiles and the scales
+  uint64_t* q_empty = full + SQ;
+  uint64_t* b_empty = q_empty + SQ;
+  uint64_t* a_full = b_empty + SQ;         // used in the first CTA
   uint64_t* a_empty = a_full + SA;
   uint64_t* tfull = a_empty + SA;
-  uint64_t* tempty = tfull + 2;
+  uint64_t* tempty = tfull + 2;            // used in the first CTA
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int units = p.tiles_m * p.tiles_n * p.splits;
   constexpr uint32_t kCols = 2 * BN;  // TMEM columns: two accumulators
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < SQ; ++s) {
-      mbar_init(q_full + s, 1);
-      mbar_init(q_empty + s, 4);
-      mbar_init(b_full + s, 1);
+      mbar_init(full + s, 1 + 32);  // the TMA producer's arrival and the scale warp's lanes
+      mbar_init(q_empty + s, kGroupWarps);
       mbar_init(b_empty + s, 1);
     }
     for (int s = 0; s < SA; ++s) {
-      mbar_init(a_full + s, 4);
+      mbar_init(a_full + s, 2 * kGroupWarps);  // of both CTAs
       mbar_init(a_empty + s, 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull + a, 1);
-      mbar_init(tempty + a, 8);
+      mbar_init(tempty + a, 2 * 8);
     }
     mbar_init(drain, 1);
     *abort = 0;
     fence_mbar_init();
   }
-  if (warp == 2) {
-    tmem_alloc(tmem_slot, kCols);
-    tmem_relinquish();
-  }
+  if (warp == 2) tmem_alloc_pair(tmem_slot, kCols);
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // the other CTA's barriers are ready
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
   if (warp < 4) {
-    reg_dec<56>();
+    reg_dec<48>();
     if (warp == 0 && lane == 0) {
       // ---------------- TMA producer
       prefetch_map(&tmQ);
@@ -161,17 +230,17 @@ __global__ void __launch_bounds__(NT, 1)
       int stage = 0, used = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      for (int u = pair; u < units && ok; u += pairs) {
         const Unit t = unit_of<BN>(p, u);
         for (int kb = t.kb0; kb < t.kb1; ++kb) {
           if (!wait_bounded(q_empty + stage, phase ^ 1, p.max_spins, abort) ||
               !wait_bounded(b_empty + stage, phase ^ 1, p.max_spins, abort)) { ok = false; break; }
-          mbar_expect_tx(q_full + stage, Q_BYTES);
-          tma_load_2d(sQ + stage * Q_BYTES, &tmQ, q_full + stage, t.m0, kb * BK);
-          mbar_expect_tx(b_full + stage, B_BYTES);
+          mbar_expect_tx(full + stage, Q_BYTES + B_BYTES);
+          tma_load_2d(sQ + stage * Q_BYTES, &tmQ, full + stage, t.m0 + rank * BM, kb * BK);
 #pragma unroll
-          for (int j = 0; j < BN / 64; ++j)
-            tma_load_2d(sB + stage * B_BYTES + j * 8192, &tmD, b_full + stage, t.n0 + 64 * j, kb * BK);
+          for (int j = 0; j < HB / 64; ++j)
+            tma_load_2d(sB + stage * B_BYTES + j * 8192, &tmD, full + stage, t.n0 + rank * HB + 64 * j,
+                        kb * BK);
           if (used < SQ) ++used;
           if (++stage == SQ) { stage = 0; phase ^= 1; }
         }
@@ -180,121 +249,170 @@ __global__ void __launch_bounds__(NT, 1)
         for (int i = 0; i < used; ++i) {
           stage = (stage + SQ - 1) % SQ;
           if (stage == SQ - 1) phase ^= 1;
-          wait_drain(q_full + stage, phase);
-          wait_drain(b_full + stage, phase);
+          wait_drain(full + stage, phase);
         }
-    } else if (warp == 1 && lane == 0) {
-      // ---------------- MMA issuer
-      constexpr uint32_t idesc = idesc_bf16(BM, BN, true, true);
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+      // ---------------- MMA issuer of the pair: a stage is ready once the converters of both
+      // CTAs, who waited for its D tile too, have arrived
+      constexpr uint32_t idesc = idesc_bf16(PM, BN, true, true);
       int sb = 0, sa = 0, acc = 0;
-      uint32_t pb = 0, pa = 0, pacc = 0;
+      uint32_t pa = 0, pacc = 0;
       bool ok = true;
-      for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      for (int u = pair; u < units && ok; u += pairs) {
         const Unit t = unit_of<BN>(p, u);
         for (int c0 = t.kb0; c0 < t.kb1 && ok; c0 += kChunk) {
           if (!wait_bounded(tempty + acc, pacc ^ 1, p.max_spins, abort)) { ok = false; break; }
           tc_fence_after();
           const int c1 = min(t.kb1, c0 + kChunk);
           for (int kb = c0; kb < c1; ++kb) {
-            if (!wait_bounded(b_full + sb, pb, p.max_spins, abort) ||
-                !wait_bounded(a_full + sa, pa, p.max_spins, abort)) { ok = false; break; }
+            if (!wait_bounded(a_full + sa, pa, p.max_spins, abort)) { ok = false; break; }
             tc_fence_after();
             const uint32_t ab = smem_u32(sA + sa * A_BYTES), bb = smem_u32(sB + sb * B_BYTES);
 #pragma unroll
             for (int k = 0; k < BK / 16; ++k)
-              mma_bf16(tmem + acc * BN, sw128_desc(ab + k * 2048, 8192, 1024),
+              mma_pair(tmem + acc * BN, sw128_desc(ab + k * 2048, 8192, 1024),
                        sw128_desc(bb + k * 2048, 8192, 1024), idesc, ((kb - c0) | k) != 0);
-            mma_commit(b_empty + sb);
-            mma_commit(a_empty + sa);
-            if (++sb == SQ) { sb = 0; pb ^= 1; }
+            commit_pair(b_empty + sb);
+            commit_pair(a_empty + sa);
+            if (++sb == SQ) sb = 0;
             if (++sa == SA) { sa = 0; pa ^= 1; }
           }
           if (!ok) break;
-          mma_commit(tfull + acc);
+          commit_pair(tfull + acc);
           acc ^= 1;
           if (acc == 0) pacc ^= 1;
         }
       }
-      mma_commit(drain);
+      asm volatile(
+          "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(drain))
+          : "memory");
       wait_drain(drain, 0);
+    } else if (warp == 3) {
+      // ---------------- scale bytes: four per token, two tokens a lane
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int u = pair; u < units && ok; u += pairs) {
+        const Unit t = unit_of<BN>(p, u);
+        const int64_t c = (t.m0 + rank * BM) / DION_ACT_BLOCK;
+        const int valid = (int)min((int64_t)4, max((int64_t)0, p.ld_scale - c));  // bytes of a token
+        for (int kb = t.kb0; kb < t.kb1; ++kb) {
+          ok = __all_sync(0xffffffffu, wait_bounded(q_empty + stage, phase ^ 1, p.max_spins, abort));
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int64_t tok = (int64_t)kb * BK + lane + 32 * i;
+            const bool in = tok < p.tokens;
+            const uint8_t* s = p.scale + (in ? tok * p.ld_scale + c : 0);
+            uint32_t* to = sS + stage * BK + lane + 32 * i;
+            if (p.scale4) {  // asynchronous: the ring's stages are all in flight
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(to)),
+                           "l"(valid == 4 ? s : p.scale), "r"(in && valid == 4 ? 4 : 0)
+                           : "memory");
+            } else {
+              uint32_t w = 0;
+#pragma unroll
+              for (int b = 0; b < 4; ++b)
+                if (in && b < valid) w |= (uint32_t)__ldg(s + b) << (8 * b);
+              *to = w;
+            }
+          }
+          if (p.scale4)
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(full + stage))
+                         : "memory");
+          else
+            mbar_arrive(full + stage);
+          if (++stage == SQ) { stage = 0; phase ^= 1; }
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");  // nothing in flight when the CTA ends
     }
-  } else if (warp < 8) {
+  } else if (warp < 4 + kGroups * kGroupWarps) {
     // ---------------- converters: 16 features of a token at a time
-    reg_dec<112>();
-    const int tid = threadIdx.x - 128;
+    reg_dec<64>();
+    const int group = (warp - 4) / kGroupWarps;
+    const int tid = (threadIdx.x - 128) % (32 * kGroupWarps);
     const int c = tid & 7;                      // features 16 c .. 16 c + 15 of the tile
     const int swap = c >= 4 ? 1 : 0;            // halves store in opposite order: no bank conflict
-    int sq = 0, sa = 0;
-    uint32_t pq = 0, pa = 0;
+    const int j0 = 2 * (c & 3) + swap, j1 = 2 * (c & 3) + 1 - swap;
+    int it = 0;                                 // stages of this CTA so far
     bool ok = true;
-    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+    for (int u = pair; u < units && ok; u += pairs) {
       const Unit t = unit_of<BN>(p, u);
-      const int64_t sc = (t.m0 + 16 * c) / 32;
-      const uint8_t* scale = p.scale + sc;
-      const bool in = sc < p.ld_scale;
-      uint32_t E[4];
-      auto scales = [&](int kb) {  // of this thread's four tokens (0: past the end)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int64_t tok = (int64_t)kb * BK + (tid >> 3) + 16 * i;
-          E[i] = in && kb < t.kb1 && tok < p.tokens ? scale[tok * p.ld_scale] : 0u;
-        }
-      };
-      scales(t.kb0);
-      for (int kb = t.kb0; kb < t.kb1; ++kb) {
-        const bool w = wait_bounded(q_full + sq, pq, p.max_spins, abort) &&
-                       wait_bounded(a_empty + sa, pa ^ 1, p.max_spins, abort);
+      for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+        if (it % kGroups != group) continue;
+        const int sq = it % SQ, sa = it % SA;
+        const bool w = wait_bounded(full + sq, (it / SQ) & 1, p.max_spins, abort) &&
+                       wait_bounded(a_empty + sa, ((it / SA) & 1) ^ 1, p.max_spins, abort);
         if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
         const uint8_t* src = sQ + sq * Q_BYTES;
+        const uint32_t* scale = sS + sq * BK;
         uint8_t* dst = sA + sa * A_BYTES + (c >> 2) * 8192;
-        uint4 raw[4];
-        uint32_t f[4];
+        uint4 raw[kItems];
+        uint32_t E[kItems];
+        bool wide = false;  // some factor 2^(E - 127 + 120) is no bf16 number: two products
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          raw[i] = *reinterpret_cast<const uint4*>(src + ((tid >> 3) + 16 * i) * BM + c * 16);
-          // 2^(E - 127) as bf16; a marked block is NaN; tokens past the end are zeros
-          const uint32_t h = E[i] == 255u ? 0x7fc0u : E[i] << 7;
-          f[i] = h | h << 16;
+        for (int i = 0; i < kItems; ++i) {
+          const int k = (tid >> 3) + 4 * kGroupWarps * i;
+          raw[i] = *reinterpret_cast<const uint4*>(src + k * BM + c * 16);
+          E[i] = scale[k] >> (8 * (c >> 1)) & 255u;
+          wide |= E[i] > 134u;
         }
-        scales(kb + 1);
+        if (__any_sync(0xffffffffu, wide)) {
+#pragma unroll 1
+          for (int i = 0; i < kItems; ++i) {
+            const int k = (tid >> 3) + 4 * kGroupWarps * i;
+            const uint4 x = *reinterpret_cast<const uint4*>(src + k * BM + c * 16);
+            const uint32_t e = scale[k] >> (8 * (c >> 1)) & 255u;
+            // a marked block is NaN; tokens past the end have no scale: zeros
+            const uint32_t f = (e == 255u ? 0x7fc0u : e << 7) * 0x10001u;
+            uint4 lo, hi;
+            const uint32_t up = 0x7b807b80u;  // 2^120
+            e4m3x4_bf16(x.x, up, lo.x, lo.y);
+            e4m3x4_bf16(x.y, up, lo.z, lo.w);
+            e4m3x4_bf16(x.z, up, hi.x, hi.y);
+            e4m3x4_bf16(x.w, up, hi.z, hi.w);
+            lo.x = bf16x2_mul(lo.x, f); lo.y = bf16x2_mul(lo.y, f);
+            lo.z = bf16x2_mul(lo.z, f); lo.w = bf16x2_mul(lo.w, f);
+            hi.x = bf16x2_mul(hi.x, f); hi.y = bf16x2_mul(hi.y, f);
+            hi.z = bf16x2_mul(hi.z, f); hi.w = bf16x2_mul(hi.w, f);
+            *reinterpret_cast<uint4*>(dst + k * 128 + ((j0 ^ (k & 7)) << 4)) = swap ? hi : lo;
+            *reinterpret_cast<uint4*>(dst + k * 128 + ((j1 ^ (k & 7)) << 4)) = swap ? lo : hi;
+          }
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = (tid >> 3) + 16 * i;
-          uint4 lo, hi;
-          lo.x = e4m3x2_bf16(raw[i].x, 0x1404, f[i]);
-          lo.y = e4m3x2_bf16(raw[i].x, 0x3424, f[i]);
-          lo.z = e4m3x2_bf16(raw[i].y, 0x1404, f[i]);
-          lo.w = e4m3x2_bf16(raw[i].y, 0x3424, f[i]);
-          hi.x = e4m3x2_bf16(raw[i].z, 0x1404, f[i]);
-          hi.y = e4m3x2_bf16(raw[i].z, 0x3424, f[i]);
-          hi.z = e4m3x2_bf16(raw[i].w, 0x1404, f[i]);
-          hi.w = e4m3x2_bf16(raw[i].w, 0x3424, f[i]);
-          const int j = 2 * (c & 3);
-          const uint4 first = swap ? hi : lo, second = swap ? lo : hi;
-          *reinterpret_cast<uint4*>(dst + k * 128 + (((j + swap) ^ (k & 7)) << 4)) = first;
-          *reinterpret_cast<uint4*>(dst + k * 128 + (((j + 1 - swap) ^ (k & 7)) << 4)) = second;
+          for (int i = 0; i < kItems; ++i) {
+            const int k = (tid >> 3) + 4 * kGroupWarps * i;
+            const uint32_t f = E[i] == 0u ? 0u : ((E[i] + 120u) << 7) * 0x10001u;
+            uint4 lo, hi;
+            e4m3x4_bf16(raw[i].x, f, lo.x, lo.y);
+            e4m3x4_bf16(raw[i].y, f, lo.z, lo.w);
+            e4m3x4_bf16(raw[i].z, f, hi.x, hi.y);
+            e4m3x4_bf16(raw[i].w, f, hi.z, hi.w);
+            *reinterpret_cast<uint4*>(dst + k * 128 + ((j0 ^ (k & 7)) << 4)) = swap ? hi : lo;
+            *reinterpret_cast<uint4*>(dst + k * 128 + ((j1 ^ (k & 7)) << 4)) = swap ? lo : hi;
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(q_empty + sq);
-          mbar_arrive(a_full + sa);
+          arrive_remote(first_cta(a_full + sa));
         }
-        if (++sq == SQ) { sq = 0; pq ^= 1; }
-        if (++sa == SA) { sa = 0; pa ^= 1; }
       }
     }
   } else {
     // ---------------- epilogue: a warp owns 32 features and half of the tile's columns
-    reg_inc<168>();
-    const int ew = warp - 8;
+    reg_inc<152>();
+    const int ew = warp - 4 - kGroups * kGroupWarps;
     const int row0 = (ew & 3) * 32;
-    constexpr int HB = BN / 2;
     const int col0 = (ew >> 2) * HB;
+    // TMEM lane to feature: the converters' order 0 2 1 3 of each four
+    const int place = (lane & ~3) | ((lane & 1) << 1) | ((lane >> 1) & 1);
     int acc = 0;
     uint32_t pacc = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+    for (int u = pair; u < units && ok; u += pairs) {
       const Unit t = unit_of<BN>(p, u);
       float run[HB];
 #pragma unroll
@@ -305,21 +423,21 @@ __global__ void __launch_bounds__(NT, 1)
         tc_fence_after();
         const uint32_t base = tmem + ((uint32_t)row0 << 16) + acc * BN + col0;
 #pragma unroll
-        for (int c = 0; c < HB; c += 16) {
-          float v[16];
-          tmem_ld16(base + c, v);
+        for (int c = 0; c < HB; c += 8) {
+          float v[8];
+          tmem_ld8(base + c, v);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) run[c + i] += v[i];
+          for (int i = 0; i < 8; ++i) run[c + i] += v[i];
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(tempty + acc);
+        if (lane == 0) arrive_remote(first_cta(tempty + acc));
         acc ^= 1;
         if (acc == 0) pacc ^= 1;
       }
       if (!ok) break;
-      const int64_t row = t.m0 + row0 + lane;
+      const int64_t row = t.m0 + rank * BM + row0 + place;
       const int64_t n0 = t.n0 + col0;
       if (row >= p.m) {
         // a lane past the last feature writes nothing
@@ -355,10 +473,12 @@ __global__ void __launch_bounds__(NT, 1)
     }
     if ((!ok || *abort) && lane == 0 && p.status) atomicOr(p.status, F_TIMEOUT);
   }
+  tc_fence_before();
   __syncthreads();
+  cluster_sync();  // neither CTA leaves while the other may still reach its memory
   if (warp == 2) {
     tc_fence_after();
-    tmem_dealloc(tmem, kCols);
+    tmem_dealloc_pair(tmem, kCols);
   }
 }
 
@@ -457,7 +577,7 @@ dion_status map2d(CUtensorMap* m, const void* base, CUtensorMapDataType type,
     if (st_ != DION_OK) return st_; \
   } while (0)
 
-constexpr int kSms = 148;  // plans (and so workspace sizes) do not depend on the device asked
+constexpr int kPairs = 74;  // of SMs; plans (and so workspace sizes) do not depend on the device asked
 
 struct GradPlan {
   int bn, tiles_m, tiles_n, splits, blocks, blocks_per_split;
@@ -471,14 +591,14 @@ size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 GradPlan plan_of(const dion_grad_source& s) {
   GradPlan g{};
   const int64_t m = s.kept.features, n = s.n;
-  g.bn = n > 128 ? 256 : n > 64 ? 128 : 64;
-  g.tiles_m = (int)((m + BM - 1) / BM);
+  g.bn = n > 128 ? 256 : 128;
+  g.tiles_m = (int)((m + PM - 1) / PM);
   g.tiles_n = (int)((n + g.bn - 1) / g.bn);
   g.blocks = (int)((s.kept.tokens + BK - 1) / BK);
-  // tokens are split where a second tile's worth of SMs would idle, whole chunks each
+  // tokens are split where a second tile's worth of pairs would idle, whole chunks each
   const int64_t tiles = (int64_t)g.tiles_m * g.tiles_n;
   const int chunks = (g.blocks + kChunk - 1) / kChunk;
-  int64_t want = tiles > 0 ? kSms / tiles : 1;
+  int64_t want = kPairs / tiles;
   if (want > chunks) want = chunks;
   if (want < 1) want = 1;
   const int per = chunks > 0 ? (int)((chunks + want - 1) / want) : 1;
@@ -504,13 +624,14 @@ dion_status check_source(const dion_grad_source& s, int i) {
 
 template <int BN>
 dion_status launch(const CUtensorMap& mq, const CUtensorMap& md, const WgradP& p, int sms, cudaStream_t s) {
-  constexpr size_t smem = 1024 + SA * A_BYTES + SQ * (BK * BN * 2 + Q_BYTES) +
-                          (4 * SQ + 2 * SA + 5) * 8 + 16;
+  constexpr size_t smem = 1024 + SA * A_BYTES + SQ * (BK * BN + Q_BYTES + BK * 4) +
+                          (3 * SQ + 2 * SA + 5) * 8 + 16;
   const cudaError_t e = cudaFuncSetAttribute(k_wgrad<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)smem);
   if (e != cudaSuccess) return set_error(DION_ERR_CUDA, "k_wgrad: %s", cudaGetErrorString(e));
   const int64_t units = (int64_t)p.tiles_m * p.tiles_n * p.splits;
-  k_wgrad<BN><<<(unsigned)(units < sms ? units : sms), NT, smem, s>>>(mq, md, p);
+  const int64_t pairs = sms / 2;
+  k_wgrad<BN><<<(unsigned)(2 * (units < pairs ? units : pairs)), NT, smem, s>>>(mq, md, p);
   return launch_status("k_wgrad");
 }
 
@@ -556,9 +677,9 @@ dion_status one_grad(const dion_grad_source& src, int accumulate, char* ws, int3
   p.transposed = src.transposed != 0;
   p.accumulate = accumulate != 0;
   p.vec = g.splits > 1 ? n % 4 == 0 : rows_aligned16(src.G, src.ldg, 4);
+  p.scale4 = p.ld_scale % 4 == 0 && aligned_to(p.scale, 4);
   p.max_spins = kMaxSpins;
-  dion_status st = g.bn == 256 ? launch<256>(mq, md, p, sms, s)
-                   : g.bn == 128 ? launch<128>(mq, md, p, sms, s) : launch<64>(mq, md, p, sms, s);
+  const dion_status st = g.bn == 256 ? launch<256>(mq, md, p, sms, s) : launch<128>(mq, md, p, sms, s);
   if (st != DION_OK || g.splits == 1) return st;
   k_wgrad_join<<<dim3((unsigned)((n + 31) / 32), (unsigned)((m + 31) / 32)), 256, 0, s>>>(
       reinterpret_cast<const float*>(ws), src.G, src.ldg, m, n, g.splits, p.transposed, p.accumulate);

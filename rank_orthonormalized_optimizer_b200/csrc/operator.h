@@ -5,17 +5,22 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <cmath>
 
 #include "internal.h"
 
 namespace dion {
 
-// The current device must be an sm_100; *sms receives its SM count.
+// The current device must be an sm_100; *sms receives its SM count.  A device is asked once:
+// what it is does not change while the process lives.
 inline dion_status check_sm100(int* sms) {
+  static std::atomic<int> known[64];  // SM count of a device found to be an sm_100
   int dev = -1;
   const cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return set_error(DION_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
+  const bool slot = dev >= 0 && dev < 64;
+  if (slot && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return DION_OK;
   int major = 0, minor = 0;
   cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
   cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
@@ -26,6 +31,7 @@ inline dion_status check_sm100(int* sms) {
   *sms = 0;
   cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
   if (*sms <= 0) *sms = 148;
+  if (slot) known[dev].store(*sms, std::memory_order_relaxed);
   return DION_OK;
 }
 

@@ -148,12 +148,13 @@ class _Bound:
 
     def _stream(self, stream):
         import torch
-        if torch.cuda.current_device() != self._device.index:
+        device = torch.cuda.current_device()
+        if device != self._device.index:
             raise ValueError(f"the plan's tensors are on {self._device}, the current device is "
-                             f"cuda:{torch.cuda.current_device()}")
-        if stream is None:
-            stream = torch.cuda.current_stream()
-        return c_void_p(stream.cuda_stream)
+                             f"cuda:{device}")
+        if stream is None:      # the handle alone: a Stream object takes longer than the launch
+            return torch._C._cuda_getCurrentRawStream(device)
+        return stream.cuda_stream
 
 
 # ------------------------------------------------------------------ activations in 8 bits
