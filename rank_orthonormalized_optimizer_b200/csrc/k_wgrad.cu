@@ -13,10 +13,10 @@
 //   warp 1        MMA issuer (one thread, in the pair's first CTA)
 //   warp 2        TMEM allocator
 //   warp 3        the tile's scale bytes (cp.async)
-//   warps 4..11   converters: e4m3 and scale -> bf16, written as the 128-byte-swizzled
-//                 MN-major operand that tcgen05.mma reads; two groups of four take every
-//                 other stage, so that one group's latencies pass behind the other's work
-//   warps 12..19  epilogue
+//   warps 4..15   converters: e4m3 and scale -> bf16, written as the 128-byte-swizzled
+//                 MN-major operand that tcgen05.mma reads; three groups of four take turns,
+//                 so that one group's latencies pass behind the others' work
+//   warps 16..23  epilogue
 // The tensor cores' accumulation rounds toward zero, which adds up over thousands of MMAs,
 // so the tokens are cut into chunks of kChunk blocks, each accumulated from zero in TMEM
 // (two accumulators in turn), and the epilogue warps add the chunks in fp32 registers.
@@ -40,10 +40,15 @@ constexpr int BM = 128;      // features of A per CTA = TMEM lanes
 constexpr int PM = 2 * BM;   // features of a pair's tile
 constexpr int BK = 64;       // tokens per stage
 constexpr int kChunk = 8;    // stages per accumulation chunk
-constexpr int NT = 640;
+constexpr int NT = 32 * (4 + 12 + 8);
 constexpr int SQ = 6;        // stages of the 8-bit and D tiles
 constexpr int SA = 4;        // stages of the converted operand
-constexpr int kGroups = 2, kGroupWarps = 4;                // converters
+constexpr int kGroups = 3, kGroupWarps = 4;                // converters
+// A converter group waits for a stage's barrier by its parity alone, so the stage that used the
+// slot before must be known to be full by then: it is the group's own when SQ is a multiple of
+// kGroups.  (Of the converted ring, a group's last wait says that all MMAs up to SA stages
+// before its last stage are done, which covers the slot's previous use when SA >= kGroups.)
+static_assert(SQ % kGroups == 0 && SA >= kGroups, "a slot's previous phase must be over");
 constexpr int kItems = BK * BM / 16 / (32 * kGroupWarps);  // 16-feature groups per thread
 constexpr int Q_BYTES = BK * BM;
 constexpr int A_BYTES = BK * BM * 2;
@@ -76,6 +81,21 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
                : "r"(taddr));
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
 }
 template <int R> __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
@@ -222,7 +242,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   const uint32_t tmem = *tmem_slot;
 
   if (warp < 4) {
-    reg_dec<48>();
+    reg_dec<40>();
     if (warp == 0 && lane == 0) {
       // ---------------- TMA producer
       prefetch_map(&tmQ);
@@ -328,70 +348,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
       asm volatile("cp.async.wait_all;" ::: "memory");  // nothing in flight when the CTA ends
     }
   } else if (warp < 4 + kGroups * kGroupWarps) {
-    // ---------------- converters: 16 features of a token at a time
-    reg_dec<64>();
+    // ---------------- converters: 16 features of a token at a time.  Eight neighbouring lanes
+    // take four 16-byte pieces of rows r and r ^ 5: under the 128-byte swizzle (piece ^ row) of
+    // both tiles, neither their loads nor their stores (every other piece) meet in a bank.
+    reg_dec<40>();
     const int group = (warp - 4) / kGroupWarps;
     const int tid = (threadIdx.x - 128) % (32 * kGroupWarps);
-    const int c = tid & 7;                      // features 16 c .. 16 c + 15 of the tile
-    const int swap = c >= 4 ? 1 : 0;            // halves store in opposite order: no bank conflict
-    const int j0 = 2 * (c & 3) + swap, j1 = 2 * (c & 3) + 1 - swap;
-    int it = 0;                                 // stages of this CTA so far
+    const int c = (tid & 3) | (tid >> 1 & 4);   // features 16 c .. 16 c + 15 of the tile
+    const int r7 = (tid >> 4 & 3) ^ (tid & 4 ? 5 : 0);
+    const int k0 = (tid >> 6) * 8 + r7;         // first token of the stage; the next are 16 apart
+    const uint32_t src0 = k0 * BM + ((c ^ r7) << 4);
+    const uint32_t dst0 = (c >> 2) * 8192 + k0 * 128 + ((2 * (c & 3) ^ r7) << 4);
+    const uint32_t base = smem_u32(smem);
+    const uint32_t byte = 0x4440 | c >> 1;      // this thread's scale byte of a token's word
+    int sq = group % SQ, sa = group % SA;
+    uint32_t pq = 0, pa = 0;
+    int skip = group;                           // stages until this group's next
     bool ok = true;
     for (int u = pair; u < units && ok; u += pairs) {
       const Unit t = unit_of<BN>(p, u);
-      for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
-        if (it % kGroups != group) continue;
-        const int sq = it % SQ, sa = it % SA;
-        const bool w = wait_bounded(full + sq, (it / SQ) & 1, p.max_spins, abort) &&
-                       wait_bounded(a_empty + sa, ((it / SA) & 1) ^ 1, p.max_spins, abort);
+      int kb = t.kb0 + skip;
+      for (; kb < t.kb1; kb += kGroups) {
+        const bool w = wait_bounded(full + sq, pq, p.max_spins, abort) &&
+                       wait_bounded(a_empty + sa, pa ^ 1, p.max_spins, abort);
         if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
-        const uint8_t* src = sQ + sq * Q_BYTES;
-        const uint32_t* scale = sS + sq * BK;
-        uint8_t* dst = sA + sa * A_BYTES + (c >> 2) * 8192;
-        uint4 raw[kItems];
-        uint32_t E[kItems];
-        bool wide = false;  // some factor 2^(E - 127 + 120) is no bf16 number: two products
+        const uint32_t src = base + (SA * A_BYTES + SQ * B_BYTES) + sq * Q_BYTES + src0;
+        const uint32_t scale = base + (SA * A_BYTES + SQ * (B_BYTES + Q_BYTES)) + (sq * BK + k0) * 4;
+        const uint32_t dst = base + sa * A_BYTES + dst0;
+        uint32_t E[kItems], top = 0;
+        uint4 next = lds128(src);
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
-          const int k = (tid >> 3) + 4 * kGroupWarps * i;
-          raw[i] = *reinterpret_cast<const uint4*>(src + k * BM + c * 16);
-          E[i] = scale[k] >> (8 * (c >> 1)) & 255u;
-          wide |= E[i] > 134u;
+          E[i] = __byte_perm(lds32(scale + 64 * i), 0, byte);
+          top = max(top, E[i]);
         }
-        if (__any_sync(0xffffffffu, wide)) {
-#pragma unroll 1
-          for (int i = 0; i < kItems; ++i) {
-            const int k = (tid >> 3) + 4 * kGroupWarps * i;
-            const uint4 x = *reinterpret_cast<const uint4*>(src + k * BM + c * 16);
-            const uint32_t e = scale[k] >> (8 * (c >> 1)) & 255u;
-            // a marked block is NaN; tokens past the end have no scale: zeros
-            const uint32_t f = (e == 255u ? 0x7fc0u : e << 7) * 0x10001u;
-            uint4 lo, hi;
-            const uint32_t up = 0x7b807b80u;  // 2^120
-            e4m3x4_bf16(x.x, up, lo.x, lo.y);
-            e4m3x4_bf16(x.y, up, lo.z, lo.w);
-            e4m3x4_bf16(x.z, up, hi.x, hi.y);
-            e4m3x4_bf16(x.w, up, hi.z, hi.w);
-            lo.x = bf16x2_mul(lo.x, f); lo.y = bf16x2_mul(lo.y, f);
-            lo.z = bf16x2_mul(lo.z, f); lo.w = bf16x2_mul(lo.w, f);
-            hi.x = bf16x2_mul(hi.x, f); hi.y = bf16x2_mul(hi.y, f);
-            hi.z = bf16x2_mul(hi.z, f); hi.w = bf16x2_mul(hi.w, f);
-            *reinterpret_cast<uint4*>(dst + k * 128 + ((j0 ^ (k & 7)) << 4)) = swap ? hi : lo;
-            *reinterpret_cast<uint4*>(dst + k * 128 + ((j1 ^ (k & 7)) << 4)) = swap ? lo : hi;
-          }
-        } else {
+        // up to E = 134 the factor 2^(E - 127) 2^120 is one bf16 number; above, two products
+        const bool wide = __any_sync(0xffffffffu, top > 134u);
 #pragma unroll
-          for (int i = 0; i < kItems; ++i) {
-            const int k = (tid >> 3) + 4 * kGroupWarps * i;
-            const uint32_t f = E[i] == 0u ? 0u : ((E[i] + 120u) << 7) * 0x10001u;
-            uint4 lo, hi;
-            e4m3x4_bf16(raw[i].x, f, lo.x, lo.y);
-            e4m3x4_bf16(raw[i].y, f, lo.z, lo.w);
-            e4m3x4_bf16(raw[i].z, f, hi.x, hi.y);
-            e4m3x4_bf16(raw[i].w, f, hi.z, hi.w);
-            *reinterpret_cast<uint4*>(dst + k * 128 + ((j0 ^ (k & 7)) << 4)) = swap ? hi : lo;
-            *reinterpret_cast<uint4*>(dst + k * 128 + ((j1 ^ (k & 7)) << 4)) = swap ? lo : hi;
+        for (int i = 0; i < kItems; ++i) {
+          const uint4 raw = next;
+          if (i + 1 < kItems) next = lds128(src + (i + 1) * 16 * BM);
+          const uint32_t f = wide ? 0x7b807b80u : E[i] * 0x00800080u + 0x3c003c00u;
+          uint4 lo, hi;
+          e4m3x4_bf16(raw.x, f, lo.x, lo.y);
+          e4m3x4_bf16(raw.y, f, lo.z, lo.w);
+          e4m3x4_bf16(raw.z, f, hi.x, hi.y);
+          e4m3x4_bf16(raw.w, f, hi.z, hi.w);
+          if (wide) {  // a marked block is NaN; tokens past the end (no scale) are zeros
+            const uint32_t g = E[i] == 255u ? 0x7fc07fc0u : E[i] * 0x00800080u;
+            lo.x = bf16x2_mul(lo.x, g); lo.y = bf16x2_mul(lo.y, g);
+            lo.z = bf16x2_mul(lo.z, g); lo.w = bf16x2_mul(lo.w, g);
+            hi.x = bf16x2_mul(hi.x, g); hi.y = bf16x2_mul(hi.y, g);
+            hi.z = bf16x2_mul(hi.z, g); hi.w = bf16x2_mul(hi.w, g);
           }
+          sts128(dst + i * 16 * 128, lo);
+          sts128((dst ^ 16) + i * 16 * 128, hi);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -399,7 +410,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
           mbar_arrive(q_empty + sq);
           arrive_remote(first_cta(a_full + sa));
         }
+        if ((sq += kGroups) >= SQ) { sq -= SQ; pq ^= 1; }
+        if ((sa += kGroups) >= SA) { sa -= SA; pa ^= 1; }
       }
+      skip = kb - t.kb1;
     }
   } else {
     // ---------------- epilogue: a warp owns 32 features and half of the tile's columns
@@ -656,7 +670,7 @@ dion_status one_grad(const dion_grad_source& src, int accumulate, char* ws, int3
   }
   const int64_t ld = kept_ld(m);
   CUtensorMap mq, md;
-  DION_TRY(map2d(&mq, src.kept.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE,
+  DION_TRY(map2d(&mq, src.kept.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B,
                  (uint64_t)ld, (uint64_t)tokens, (uint64_t)ld, BM, BK));
   DION_TRY(map2d(&md, d, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, (uint64_t)n,
                  (uint64_t)tokens, (uint64_t)ldd * 2, 64, BK));
