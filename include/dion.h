@@ -498,8 +498,8 @@ typedef struct dion_grad_source {
   int32_t transposed;
 } dion_grad_source;
 
-/* Bytes of workspace for a list of sources (they take turns in it); 0 when none is needed
- * or the sources are invalid. */
+/* Bytes of workspace for a list of sources (they take turns in it), from their shapes and d's
+ * alignment; 0 when none is needed or a shape is not supported. */
 size_t dion_weight_grad_workspace(const dion_grad_source* sources, int32_t nsources);
 
 /* Every gradient of the list, one after the other.  d_status (may be NULL): device int32,

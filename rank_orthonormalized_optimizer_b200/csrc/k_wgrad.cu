@@ -9,9 +9,9 @@
 // fp32 additions.  The contraction over the tokens runs on the tensor cores: a persistent pair
 // of CTAs (a cluster, tcgen05 cta_group::2) owns 256 x BN tiles of G, each CTA 128 of the
 // features and half of the columns, and walks the tokens 64 at a time.  In each CTA
-//   warp 0        TMA producer: the 8-bit tile (64 tokens x 128 features), half of the D tile
+//   warp 0        TMA producer of the 8-bit tile (64 tokens x 128 features)
 //   warp 1        MMA issuer (one thread, in the pair's first CTA)
-//   warp 2        TMEM allocator
+//   warp 2        TMEM allocator; TMA producer of the CTA's half of the D tile
 //   warp 3        the tile's scale bytes (cp.async)
 //   warps 4..15   converters: e4m3 and scale -> bf16, written as the 128-byte-swizzled
 //                 MN-major operand that tcgen05.mma reads; three groups of four take turns,
@@ -20,11 +20,12 @@
 // The tensor cores' accumulation rounds toward zero, which adds up over thousands of MMAs,
 // so the tokens are cut into chunks of kChunk blocks, each accumulated from zero in TMEM
 // (two accumulators in turn), and the epilogue warps add the chunks in fp32 registers.
-// Where the tiles are fewer than the pairs the tokens are also split over pairs; the partial
-// sums go to the workspace and a second kernel adds them in order.  Every wait is bounded.
+// The tiles that do not fill a last round over all pairs (all of them, in a small matrix) are
+// also split over the tokens, so that every pair has a share; their partial sums go to the
+// workspace and a second kernel adds them in order.  Every wait is bounded.
 #include <cuda.h>
 
-#include <cstdio>
+#include <algorithm>
 
 #include "common.cuh"
 #include "operator.h"
@@ -41,14 +42,16 @@ constexpr int PM = 2 * BM;   // features of a pair's tile
 constexpr int BK = 64;       // tokens per stage
 constexpr int kChunk = 8;    // stages per accumulation chunk
 constexpr int NT = 32 * (4 + 12 + 8);
-constexpr int SQ = 6;        // stages of the 8-bit and D tiles
+constexpr int SQ = 6;        // stages of the 8-bit tiles
+constexpr int SB = 6;        // stages of the D tiles
 constexpr int SA = 4;        // stages of the converted operand
 constexpr int kGroups = 3, kGroupWarps = 4;                // converters
 // A converter group waits for a stage's barrier by its parity alone, so the stage that used the
 // slot before must be known to be full by then: it is the group's own when SQ is a multiple of
 // kGroups.  (Of the converted ring, a group's last wait says that all MMAs up to SA stages
-// before its last stage are done, which covers the slot's previous use when SA >= kGroups.)
-static_assert(SQ % kGroups == 0 && SA >= kGroups, "a slot's previous phase must be over");
+// before its last stage are done, which covers the slot's previous use when SA >= kGroups;
+// the MMAs it knows done had their D tiles, which covers D's slots when SB >= SA.)
+static_assert(SQ % kGroups == 0 && SA >= kGroups && SB >= SA, "a slot's previous phase must be over");
 constexpr int kItems = BK * BM / 16 / (32 * kGroupWarps);  // 16-feature groups per thread
 constexpr int Q_BYTES = BK * BM;
 constexpr int A_BYTES = BK * BM * 2;
@@ -56,10 +59,12 @@ constexpr int64_t kMaxSpins = int64_t(1) << 26;
 
 struct WgradP {
   const uint8_t* scale;
-  float* out;        // G, or the partial sums [splits][m][n] (row-major always)
+  float* out;        // G
+  float* parts;      // [tail tile][split][PM][BN]: partial sums of the split tiles
   int32_t* status;
   int64_t tokens, ld_scale, ldg, m, n;
-  int tiles_m, tiles_n, splits, blocks_per_split, blocks;  // blocks: of 64 tokens
+  int tiles_m, whole, tail;               // tiles taken whole, and split over the tokens
+  int splits, blocks_per_split, blocks;   // blocks: of 64 tokens
   int transposed, accumulate, vec;
   int scale4;        // the scale bytes of a tile's token are an aligned word
   int64_t max_spins;
@@ -170,20 +175,26 @@ __device__ __forceinline__ void e4m3x4_bf16(uint32_t w, uint32_t f, uint32_t& ev
   odd = bf16x2_mul(((w >> 4) & M) | (s & ~M), f);
 }
 
-// A unit of work: one tile over one range of token blocks.
+// A unit of work: one tile over one range of token blocks; part: where its partial sums go
+// (-1: the whole sum, straight to G).
 struct Unit {
-  int m0, n0, split, kb0, kb1;
+  int m0, n0, part, kb0, kb1;
 };
 template <int BN>
 __device__ __forceinline__ Unit unit_of(const WgradP& p, int u) {
   Unit t;
-  const int tiles = p.tiles_m * p.tiles_n;
-  t.split = u / tiles;
-  const int rem = u - t.split * tiles;
-  t.m0 = (rem % p.tiles_m) * PM;
-  t.n0 = (rem / p.tiles_m) * BN;
-  t.kb0 = t.split * p.blocks_per_split;
-  t.kb1 = min(p.blocks, t.kb0 + p.blocks_per_split);
+  int tile = u;
+  t.part = -1;
+  t.kb0 = 0;
+  t.kb1 = p.blocks;
+  if (u >= p.whole) {
+    t.part = u - p.whole;
+    tile = p.whole + t.part / p.splits;
+    t.kb0 = t.part % p.splits * p.blocks_per_split;
+    t.kb1 = min(p.blocks, t.kb0 + p.blocks_per_split);
+  }
+  t.m0 = tile % p.tiles_m * PM;
+  t.n0 = tile / p.tiles_m * BN;
   return t;
 }
 
@@ -197,12 +208,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   uint8_t* smem = align1024(smem_raw);     // the same offset in both CTAs
   uint8_t* sA = smem;
   uint8_t* sB = sA + SA * A_BYTES;
-  uint8_t* sQ = sB + SQ * B_BYTES;
+  uint8_t* sQ = sB + SB * B_BYTES;
   uint32_t* sS = reinterpret_cast<uint32_t*>(sQ + SQ * Q_BYTES);  // [stage][token]: 4 scale bytes
-  uint64_t* full = reinterpret_cast<uint64_t*>(sS + SQ * BK);     // both tiles and the scales
-  uint64_t* q_empty = full + SQ;
-  uint64_t* b_empty = q_empty + SQ;
-  uint64_t* a_full = b_empty + SQ;         // used in the first CTA
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(sS + SQ * BK);   // the 8-bit tile and its scales
+  uint64_t* q_empty = q_full + SQ;
+  uint64_t* b_full = q_empty + SQ;
+  uint64_t* b_empty = b_full + SB;
+  uint64_t* a_full = b_empty + SB;         // used in the first CTA
   uint64_t* a_empty = a_full + SA;
   uint64_t* tfull = a_empty + SA;
   uint64_t* tempty = tfull + 2;            // used in the first CTA
@@ -213,13 +225,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int units = p.tiles_m * p.tiles_n * p.splits;
+  const int units = p.whole + p.tail * p.splits;
   constexpr uint32_t kCols = 2 * BN;  // TMEM columns: two accumulators
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < SQ; ++s) {
-      mbar_init(full + s, 1 + 32);  // the TMA producer's arrival and the scale warp's lanes
+      mbar_init(q_full + s, 1 + 32);  // the TMA producer's arrival and the scale warp's lanes
       mbar_init(q_empty + s, kGroupWarps);
+    }
+    for (int s = 0; s < SB; ++s) {
+      mbar_init(b_full + s, 1);
       mbar_init(b_empty + s, 1);
     }
     for (int s = 0; s < SA; ++s) {
@@ -243,33 +258,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
 
   if (warp < 4) {
     reg_dec<40>();
-    if (warp == 0 && lane == 0) {
-      // ---------------- TMA producer
-      prefetch_map(&tmQ);
-      prefetch_map(&tmD);
+    if ((warp == 0 || warp == 2) && lane == 0) {
+      // ---------------- TMA producers, one for each operand: the 8-bit tiles must not wait for
+      // the MMAs that hold D's slots, since they have to be converted first
+      const bool q = warp == 0;
+      const CUtensorMap* map = q ? &tmQ : &tmD;
+      uint64_t *fullb = q ? q_full : b_full, *emptyb = q ? q_empty : b_empty;
+      const int stages = q ? SQ : SB;
+      prefetch_map(map);
       int stage = 0, used = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int u = pair; u < units && ok; u += pairs) {
         const Unit t = unit_of<BN>(p, u);
         for (int kb = t.kb0; kb < t.kb1; ++kb) {
-          if (!wait_bounded(q_empty + stage, phase ^ 1, p.max_spins, abort) ||
-              !wait_bounded(b_empty + stage, phase ^ 1, p.max_spins, abort)) { ok = false; break; }
-          mbar_expect_tx(full + stage, Q_BYTES + B_BYTES);
-          tma_load_2d(sQ + stage * Q_BYTES, &tmQ, full + stage, t.m0 + rank * BM, kb * BK);
+          if (!wait_bounded(emptyb + stage, phase ^ 1, p.max_spins, abort)) { ok = false; break; }
+          mbar_expect_tx(fullb + stage, q ? Q_BYTES : B_BYTES);
+          if (q) {
+            tma_load_2d(sQ + stage * Q_BYTES, map, fullb + stage, t.m0 + rank * BM, kb * BK);
+          } else {
 #pragma unroll
-          for (int j = 0; j < HB / 64; ++j)
-            tma_load_2d(sB + stage * B_BYTES + j * 8192, &tmD, full + stage, t.n0 + rank * HB + 64 * j,
-                        kb * BK);
-          if (used < SQ) ++used;
-          if (++stage == SQ) { stage = 0; phase ^= 1; }
+            for (int j = 0; j < HB / 64; ++j)
+              tma_load_2d(sB + stage * B_BYTES + j * 8192, map, fullb + stage,
+                          t.n0 + rank * HB + 64 * j, kb * BK);
+          }
+          if (used < stages) ++used;
+          if (++stage == stages) { stage = 0; phase ^= 1; }
         }
       }
       if (*abort)  // let every load already issued land before the CTA goes away
         for (int i = 0; i < used; ++i) {
-          stage = (stage + SQ - 1) % SQ;
-          if (stage == SQ - 1) phase ^= 1;
-          wait_drain(full + stage, phase);
+          stage = (stage + stages - 1) % stages;
+          if (stage == stages - 1) phase ^= 1;
+          wait_drain(fullb + stage, phase);
         }
     } else if (warp == 1 && lane == 0 && rank == 0) {
       // ---------------- MMA issuer of the pair: a stage is ready once the converters of both
@@ -294,7 +315,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
                        sw128_desc(bb + k * 2048, 8192, 1024), idesc, ((kb - c0) | k) != 0);
             commit_pair(b_empty + sb);
             commit_pair(a_empty + sa);
-            if (++sb == SQ) sb = 0;
+            if (++sb == SB) sb = 0;
             if (++sa == SA) { sa = 0; pa ^= 1; }
           }
           if (!ok) break;
@@ -338,10 +359,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
             }
           }
           if (p.scale4)
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(full + stage))
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(q_full + stage))
                          : "memory");
           else
-            mbar_arrive(full + stage);
+            mbar_arrive(q_full + stage);
           if (++stage == SQ) { stage = 0; phase ^= 1; }
         }
       }
@@ -361,19 +382,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
     const uint32_t dst0 = (c >> 2) * 8192 + k0 * 128 + ((2 * (c & 3) ^ r7) << 4);
     const uint32_t base = smem_u32(smem);
     const uint32_t byte = 0x4440 | c >> 1;      // this thread's scale byte of a token's word
-    int sq = group % SQ, sa = group % SA;
-    uint32_t pq = 0, pa = 0;
+    int sq = group % SQ, sa = group % SA, sb = group % SB;
+    uint32_t pq = 0, pa = 0, pb = 0;
     int skip = group;                           // stages until this group's next
     bool ok = true;
     for (int u = pair; u < units && ok; u += pairs) {
       const Unit t = unit_of<BN>(p, u);
       int kb = t.kb0 + skip;
       for (; kb < t.kb1; kb += kGroups) {
-        const bool w = wait_bounded(full + sq, pq, p.max_spins, abort) &&
+        const bool w = wait_bounded(q_full + sq, pq, p.max_spins, abort) &&
                        wait_bounded(a_empty + sa, pa ^ 1, p.max_spins, abort);
         if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
-        const uint32_t src = base + (SA * A_BYTES + SQ * B_BYTES) + sq * Q_BYTES + src0;
-        const uint32_t scale = base + (SA * A_BYTES + SQ * (B_BYTES + Q_BYTES)) + (sq * BK + k0) * 4;
+        const uint32_t src = base + (SA * A_BYTES + SB * B_BYTES) + sq * Q_BYTES + src0;
+        const uint32_t scale = base + (SA * A_BYTES + SB * B_BYTES + SQ * Q_BYTES) + (sq * BK + k0) * 4;
         const uint32_t dst = base + sa * A_BYTES + dst0;
         uint32_t E[kItems], top = 0;
         uint4 next = lds128(src);
@@ -406,10 +427,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
+        // the arrival at the issuer says that this CTA's part of D is there, too
+        bool there = true;
         if (lane == 0) {
           mbar_arrive(q_empty + sq);
-          arrive_remote(first_cta(a_full + sa));
+          there = wait_bounded(b_full + sb, pb, p.max_spins, abort);
+          if (there) arrive_remote(first_cta(a_full + sa));
         }
+        if (!__all_sync(0xffffffffu, there)) { ok = false; break; }
+        if ((sb += kGroups) >= SB) { sb -= SB; pb ^= 1; }
         if ((sq += kGroups) >= SQ) { sq -= SQ; pq ^= 1; }
         if ((sa += kGroups) >= SA) { sa -= SA; pa ^= 1; }
       }
@@ -453,9 +479,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
       if (!ok) break;
       const int64_t row = t.m0 + rank * BM + row0 + place;
       const int64_t n0 = t.n0 + col0;
-      if (row >= p.m) {
+      if (t.part >= 0) {
+        float* g = p.parts + ((int64_t)t.part * PM + rank * BM + row0 + place) * BN + col0;
+#pragma unroll
+        for (int i = 0; i < HB; i += 4)
+          *reinterpret_cast<float4*>(g + i) = make_float4(run[i], run[i + 1], run[i + 2], run[i + 3]);
+      } else if (row >= p.m) {
         // a lane past the last feature writes nothing
-      } else if (p.transposed && p.splits == 1) {
+      } else if (p.transposed) {
         // 32 lanes write 32 neighbouring features of one column
 #pragma unroll
         for (int i = 0; i < HB; ++i)
@@ -464,14 +495,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
             *g = run[i] + (p.accumulate ? *g : 0.f);
           }
       } else {
-        const bool part = p.splits > 1;
-        float* g = part ? p.out + ((int64_t)t.split * p.m + row) * p.n + n0 : p.out + row * p.ldg + n0;
-        const bool add = p.accumulate && !part;
+        float* g = p.out + row * p.ldg + n0;
 #pragma unroll
         for (int i = 0; i < HB; i += 4) {
           if (p.vec && n0 + i + 3 < p.n) {
             float4 o = make_float4(run[i], run[i + 1], run[i + 2], run[i + 3]);
-            if (add) {
+            if (p.accumulate) {
               const float4 a = *reinterpret_cast<const float4*>(g + i);
               o.x += a.x; o.y += a.y; o.z += a.z; o.w += a.w;
             }
@@ -479,7 +508,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
           } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              if (n0 + i + j < p.n) g[i + j] = run[i + j] + (add ? g[i + j] : 0.f);
+              if (n0 + i + j < p.n) g[i + j] = run[i + j] + (p.accumulate ? g[i + j] : 0.f);
           }
         }
       }
@@ -496,35 +525,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   }
 }
 
-// Adds the splits' partial sums in order, into G in either layout.
-__global__ void __launch_bounds__(256) k_wgrad_join(const float* parts, float* G, int64_t ldg,
-                                                    int64_t m, int64_t n, int splits, int transposed,
-                                                    int accumulate) {
-  __shared__ float tile[32][33];
+// Adds the split tiles' partial sums in order, into G in either layout: 32 x 32 of a tile.
+__global__ void __launch_bounds__(256) k_wgrad_join(const WgradP p, int bn) {
+  __shared__ float block[32][33];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int64_t i0 = (int64_t)blockIdx.y * 32, j0 = (int64_t)blockIdx.x * 32;
+  const int tile = p.whole + blockIdx.z;
+  const int i0 = blockIdx.y * 32, j0 = blockIdx.x * 32;
+  const int64_t row0 = (int64_t)(tile % p.tiles_m) * PM + i0, col0 = (int64_t)(tile / p.tiles_m) * bn + j0;
+  if (row0 >= p.m || col0 >= p.n) return;
+  const int64_t plane = (int64_t)PM * bn;
+  const float* from = p.parts + blockIdx.z * p.splits * plane + (int64_t)i0 * bn + j0;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = 0; s < p.splits; ++s)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sum[k] += from[s * plane + (ty + 8 * k) * bn + tx];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int64_t i = i0 + ty + 8 * k, j = j0 + tx;
-    float a = 0.f;
-    if (i < m && j < n) {
-#pragma unroll 4
-      for (int s = 0; s < splits; ++s) a += parts[((int64_t)s * m + i) * n + j];
-      if (!transposed) {
-        float* g = G + i * ldg + j;
-        *g = a + (accumulate ? *g : 0.f);
-      }
+    const int64_t i = row0 + ty + 8 * k, j = col0 + tx;
+    if (!p.transposed && i < p.m && j < p.n) {
+      float* g = p.out + i * p.ldg + j;
+      *g = sum[k] + (p.accumulate ? *g : 0.f);
     }
-    tile[ty + 8 * k][tx] = a;
+    block[ty + 8 * k][tx] = sum[k];
   }
-  if (!transposed) return;
+  if (!p.transposed) return;
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int64_t j = j0 + ty + 8 * k, i = i0 + tx;
-    if (i < m && j < n) {
-      float* g = G + j * ldg + i;
-      *g = tile[tx][ty + 8 * k] + (accumulate ? *g : 0.f);
+    const int64_t j = col0 + ty + 8 * k, i = row0 + tx;
+    if (i < p.m && j < p.n) {
+      float* g = p.out + j * p.ldg + i;
+      *g = block[tx][ty + 8 * k] + (p.accumulate ? *g : 0.f);
     }
   }
 }
@@ -591,10 +623,12 @@ dion_status map2d(CUtensorMap* m, const void* base, CUtensorMapDataType type,
     if (st_ != DION_OK) return st_; \
   } while (0)
 
-constexpr int kPairs = 74;  // of SMs; plans (and so workspace sizes) do not depend on the device asked
+// Pairs of SMs, and the fewest blocks in a split: below two, a pair's start and the join cost
+// more than the tokens.  Plans (and so workspace sizes) do not depend on the device asked.
+constexpr int kPairs = 74, kMinBlocks = 2;
 
 struct GradPlan {
-  int bn, tiles_m, tiles_n, splits, blocks, blocks_per_split;
+  int bn, tiles_m, whole, tail, splits, blocks, blocks_per_split;
   bool pad;
   int64_t ldd;          // of the padded copy
   size_t parts_bytes, pad_bytes;
@@ -607,30 +641,41 @@ GradPlan plan_of(const dion_grad_source& s) {
   const int64_t m = s.kept.features, n = s.n;
   g.bn = n > 128 ? 256 : 128;
   g.tiles_m = (int)((m + PM - 1) / PM);
-  g.tiles_n = (int)((n + g.bn - 1) / g.bn);
   g.blocks = (int)((s.kept.tokens + BK - 1) / BK);
-  // tokens are split where a second tile's worth of pairs would idle, whole chunks each
-  const int64_t tiles = (int64_t)g.tiles_m * g.tiles_n;
-  const int chunks = (g.blocks + kChunk - 1) / kChunk;
-  int64_t want = kPairs / tiles;
-  if (want > chunks) want = chunks;
-  if (want < 1) want = 1;
-  const int per = chunks > 0 ? (int)((chunks + want - 1) / want) : 1;
-  g.blocks_per_split = per * kChunk;
-  g.splits = chunks > 0 ? (chunks + per - 1) / per : 1;
+  const int64_t tiles = g.tiles_m * ((n + g.bn - 1) / g.bn);
+  const int64_t tail = tiles % kPairs;
+  // the last, partial round is split so that it takes 1 / splits of a round
+  int64_t want = tail > 0 ? kPairs / tail : 1;
+  want = std::min<int64_t>(want, g.blocks / kMinBlocks);
+  g.splits = 1;
+  if (want > 1) {
+    g.blocks_per_split = (int)((g.blocks + want - 1) / want);
+    g.splits = (g.blocks + g.blocks_per_split - 1) / g.blocks_per_split;
+  }
+  g.tail = g.splits > 1 ? (int)tail : 0;
+  g.whole = (int)(tiles - g.tail);
   g.pad = !rows_aligned16(s.d, s.ldd, 2);
   g.ldd = (n + 7) / 8 * 8;
-  g.parts_bytes = g.splits > 1 ? up256((size_t)g.splits * m * n * 4) : 0;
+  g.parts_bytes = (size_t)g.tail * g.splits * PM * g.bn * 4;
   g.pad_bytes = g.pad ? up256((size_t)s.kept.tokens * g.ldd * 2) : 0;
   return g;
 }
 
-dion_status check_source(const dion_grad_source& s, int i) {
-  DION_TRY(check_kept(s.kept));
-  if (s.kept.features > (1 << 24) || s.n < 1 || s.n > (1 << 24))
+dion_status check_shape(const dion_grad_source& s, int i) {
+  DION_TRY(check_tokens(s.kept.tokens));
+  const int64_t m = s.kept.features;
+  if (m < 1 || m > (1 << 24) || s.n < 1 || s.n > (1 << 24))
     return set_error(DION_ERR_UNSUPPORTED_SHAPE, "source %d: m and n must lie in [1, 2^24]", i);
-  if (s.kept.tokens > INT32_MAX - BK * kChunk)
+  if ((m / PM + 1) * (s.n / 128 + 1) > (1 << 30))
+    return set_error(DION_ERR_UNSUPPORTED_SHAPE, "source %d: m n is too large", i);
+  if (s.kept.tokens > INT32_MAX - BK)
     return set_error(DION_ERR_UNSUPPORTED_SHAPE, "source %d: too many tokens", i);
+  return DION_OK;
+}
+
+dion_status check_source(const dion_grad_source& s, int i) {
+  DION_TRY(check_shape(s, i));
+  DION_TRY(check_kept(s.kept));
   if (s.kept.tokens > 0) DION_TRY(check_rows("d", s.d, s.ldd, s.n, 2));
   DION_TRY(check_rows("G", s.G, s.ldg, s.transposed ? s.kept.features : s.n, 4));
   return DION_OK;
@@ -638,12 +683,12 @@ dion_status check_source(const dion_grad_source& s, int i) {
 
 template <int BN>
 dion_status launch(const CUtensorMap& mq, const CUtensorMap& md, const WgradP& p, int sms, cudaStream_t s) {
-  constexpr size_t smem = 1024 + SA * A_BYTES + SQ * (BK * BN + Q_BYTES + BK * 4) +
-                          (3 * SQ + 2 * SA + 5) * 8 + 16;
+  constexpr size_t smem = 1024 + SA * A_BYTES + SB * BK * BN + SQ * (Q_BYTES + BK * 4) +
+                          (2 * SQ + 2 * SB + 2 * SA + 5) * 8 + 16;
   const cudaError_t e = cudaFuncSetAttribute(k_wgrad<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)smem);
   if (e != cudaSuccess) return set_error(DION_ERR_CUDA, "k_wgrad: %s", cudaGetErrorString(e));
-  const int64_t units = (int64_t)p.tiles_m * p.tiles_n * p.splits;
+  const int64_t units = p.whole + (int64_t)p.tail * p.splits;
   const int64_t pairs = sms / 2;
   k_wgrad<BN><<<(unsigned)(2 * (units < pairs ? units : pairs)), NT, smem, s>>>(mq, md, p);
   return launch_status("k_wgrad");
@@ -676,7 +721,8 @@ dion_status one_grad(const dion_grad_source& src, int accumulate, char* ws, int3
                  (uint64_t)tokens, (uint64_t)ldd * 2, 64, BK));
   WgradP p{};
   p.scale = src.kept.scale;
-  p.out = g.splits > 1 ? reinterpret_cast<float*>(ws) : src.G;
+  p.out = src.G;
+  p.parts = reinterpret_cast<float*>(ws);
   p.status = status;
   p.tokens = tokens;
   p.ld_scale = ld / DION_ACT_BLOCK;
@@ -684,19 +730,19 @@ dion_status one_grad(const dion_grad_source& src, int accumulate, char* ws, int3
   p.m = m;
   p.n = n;
   p.tiles_m = g.tiles_m;
-  p.tiles_n = g.tiles_n;
+  p.whole = g.whole;
+  p.tail = g.tail;
   p.splits = g.splits;
   p.blocks = g.blocks;
   p.blocks_per_split = g.blocks_per_split;
   p.transposed = src.transposed != 0;
   p.accumulate = accumulate != 0;
-  p.vec = g.splits > 1 ? n % 4 == 0 : rows_aligned16(src.G, src.ldg, 4);
+  p.vec = rows_aligned16(src.G, src.ldg, 4);
   p.scale4 = p.ld_scale % 4 == 0 && aligned_to(p.scale, 4);
   p.max_spins = kMaxSpins;
   const dion_status st = g.bn == 256 ? launch<256>(mq, md, p, sms, s) : launch<128>(mq, md, p, sms, s);
-  if (st != DION_OK || g.splits == 1) return st;
-  k_wgrad_join<<<dim3((unsigned)((n + 31) / 32), (unsigned)((m + 31) / 32)), 256, 0, s>>>(
-      reinterpret_cast<const float*>(ws), src.G, src.ldg, m, n, g.splits, p.transposed, p.accumulate);
+  if (st != DION_OK || g.tail == 0) return st;
+  k_wgrad_join<<<dim3((unsigned)(g.bn / 32), PM / 32, (unsigned)g.tail), 256, 0, s>>>(p, g.bn);
   return launch_status("k_wgrad_join");
 }
 
@@ -728,7 +774,7 @@ extern "C" {
 size_t dion_weight_grad_workspace(const dion_grad_source* sources, int32_t nsources) {
   size_t most = 0;
   for (int32_t i = 0; sources && i < nsources; ++i) {
-    if (dion::check_source(sources[i], i) != DION_OK) return 0;
+    if (dion::check_shape(sources[i], i) != DION_OK) return 0;
     const dion::GradPlan g = dion::plan_of(sources[i]);
     const size_t b = g.parts_bytes + g.pad_bytes;
     most = b > most ? b : most;

@@ -174,7 +174,11 @@ def test_weight_grad_list_refusals():
     assert gr.dion_weight_grad(two, -1, 0, None, 0, None, None) == dion.ERR_INVALID_ARG
     assert gr.dion_weight_grad(None, 1, 0, None, 0, None, None) == dion.ERR_INVALID_ARG
     assert gr.dion_weight_grad(two, 1, 0, None, 0, FAKE + 2, None) == dion.ERR_MISALIGNED
-    assert gr.dion_weight_grad_workspace(two, 2) == 0
+    huge = (gr.GradSource * 1)(_source(n=(1 << 24) + 1))
+    assert gr.dion_weight_grad_workspace(huge, 1) == 0
+    # the size goes by the shapes: G need not be there yet
+    no_g = _source(kept=_kept(tokens=1 << 14), G=None)
+    assert gr.dion_weight_grad_workspace(ctypes.byref(no_g), 1) > 0
     # few tiles over many tokens: the split over the tokens needs a workspace
     long = _source(kept=_kept(tokens=1 << 14))
     need = gr.dion_weight_grad_workspace(ctypes.byref(long), 1)
