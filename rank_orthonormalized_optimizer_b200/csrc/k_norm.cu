@@ -13,21 +13,32 @@
 //   dpre_gain = sum_t du hn;  S = sum_t g yn (y without the post norm)
 //   dpost_gain = s gate S;    dgate = s post_gain S     (one column sum gives both)
 //
-// Both passes are bound by HBM: every row is read once, held in registers between the row
-// sums, and written once.  The forward pass takes a row per CTA (four rows, a warp each,
-// up to 1024 features); the gains then come from L1, which the rows are loaded past.  The
-// backward pass walks rows with a fixed grid and keeps each thread's column sums in
-// registers; a second kernel adds the CTAs' partial sums in a fixed order, so results
-// repeat bit for bit.  All sums are fp32; only the stored rows are rounded.
+// Both passes are bound by HBM: every row is read once and written once, and lives in the
+// registers or the shared memory of the threads that own its columns in between.  A batch is
+// streamed: a fixed grid walks the rows, each thread fetching its own columns of the rows to
+// come into a ring of shared memory (cp.async; no thread reads another's slots, so the ring
+// needs no barrier) while it works on the current one, with its gains in registers.  A few
+// tokens, unaligned rows, and rows too wide for the ring are loaded directly, a row per CTA
+// (four rows, a warp each, up to 512 features).  The backward pass keeps each thread's column
+// sums over its rows; a second kernel adds the CTAs' sums in a fixed order, so results repeat
+// bit for bit.  All sums are fp32; only the stored rows are rounded.
 #include "operator.h"
 #include "rows.cuh"
+
+#include <algorithm>
+#include <type_traits>
 
 namespace dion {
 namespace {
 
 constexpr int64_t kMaxFeatures = 16384;  // a row stays in the registers of one CTA
 constexpr int kWarpRows = 4;             // rows of a CTA in the warp-per-row form
-constexpr int kParts = 296;              // backward: CTAs, and partial column sums, at most
+constexpr int kSms = 148;                // grids (and so workspace sizes) do not depend on the device
+constexpr int kSmemMost = 226 * 1024;    // of the rings of one SM's CTAs
+
+// Threads of a CTA, and CTAs of a streaming grid on an SM (512 threads of 128 registers).
+constexpr int cta_threads(int nt) { return nt == 32 ? 32 * kWarpRows : nt; }
+constexpr int ctas_per_sm(int nt) { return 512 / cta_threads(nt); }
 
 struct NormP {
   const void *x, *y;
@@ -144,8 +155,29 @@ __device__ __forceinline__ void gains(const float* g, int tid, int k, int d, flo
   }
 }
 
+// Eight values of a row's 8-bit form, from column c; four neighbouring lanes hold a block, and
+// every lane of the warp calls.
+__device__ __forceinline__ void keep8(uint8_t* q, uint8_t* scale, int c, int ldq, const float* v) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) top = max(top, abs_bits(v[j]));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  if (c >= ldq) return;
+  const int e = act_exponent(top);
+  const float f = act_unscale(e);
+  const bool fine = top < kInfBits;
+  uint2 o = make_uint2(0, 0);
+  if (fine) {
+    o.x = e4m3x2(v[0] * f, v[1] * f) | e4m3x2(v[2] * f, v[3] * f) << 16;
+    o.y = e4m3x2(v[4] * f, v[5] * f) | e4m3x2(v[6] * f, v[7] * f) << 16;
+  }
+  *reinterpret_cast<uint2*>(q + c) = o;
+  if ((c & 31) == 0) scale[c / 32] = fine ? e + 127 : 255;
+}
+
 template <typename T, int NT, int VPT, bool AL>
-__global__ void __launch_bounds__(NT == 32 ? 32 * kWarpRows : NT) k_norm(const NormP p) {
+__global__ void __launch_bounds__(cta_threads(NT)) k_norm(const NormP p) {
   constexpr int E = 8 * VPT;
   __shared__ float red[NT == 32 ? 1 : NT / 32];
   const int tid = NT == 32 ? threadIdx.x & 31 : threadIdx.x;
@@ -197,26 +229,10 @@ __global__ void __launch_bounds__(NT == 32 ? 32 * kWarpRows : NT) k_norm(const N
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int c = (k * NT + tid) * 8;
-      if (c >= d)  // the row's end inside the vector, and the padding of its last block
+      if (c >= d)  // the row's end inside its last block
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[8 * k + j] = 0.f;
-      uint32_t top = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) top = max(top, abs_bits(h[8 * k + j]));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      if (c >= p.ldq) continue;
-      const int e = act_exponent(top);
-      const float f = act_unscale(e);
-      const bool fine = top < kInfBits;
-      uint2 o = make_uint2(0, 0);
-      const float* v = h + 8 * k;
-      if (fine) {
-        o.x = e4m3x2(v[0] * f, v[1] * f) | e4m3x2(v[2] * f, v[3] * f) << 16;
-        o.y = e4m3x2(v[4] * f, v[5] * f) | e4m3x2(v[6] * f, v[7] * f) << 16;
-      }
-      *reinterpret_cast<uint2*>(q + c) = o;
-      if ((tid & 3) == 0) scale[c / 32] = fine ? e + 127 : 255;
+      keep8(q, scale, c, (int)p.ldq, h + 8 * k);
     }
   } else {
 #pragma unroll
@@ -233,17 +249,328 @@ __global__ void __launch_bounds__(NT == 32 ? 32 * kWarpRows : NT) k_norm(const N
   }
 }
 
+// ---- the ring: this thread's 8-element pieces of A arrays of a row, STAGES rows
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+template <typename T, int NT, int VPT, int A>
+struct Ring {
+  static constexpr int kPiece = 8 * sizeof(T);
+  static constexpr int kThreads = cta_threads(NT);
+  static constexpr int kStage = A * VPT * kPiece * kThreads;
+  uint32_t base;  // of this thread's slots: 16-byte slots of neighbouring threads lie together
+  __device__ __forceinline__ explicit Ring(void* smem) {
+    base = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + threadIdx.x * 16;
+  }
+  __device__ __forceinline__ uint32_t slot(int stage, int array, int k, int half) const {
+    return base + stage * kStage + ((array * VPT + k) * (kPiece / 16) + half) * 16 * kThreads;
+  }
+  __device__ __forceinline__ void fetch(int stage, int array, const T* row, int tid, int d) const {
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int c = (k * NT + tid) * 8;
+      if (c < d)
+#pragma unroll
+        for (int i = 0; i < kPiece / 16; ++i) copy16(slot(stage, array, k, i), row + c + i * (16 / sizeof(T)));
+    }
+  }
+  __device__ __forceinline__ uint4 read16(uint32_t a) const {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+  }
+  // piece k as 8 floats, zeros past the row's end
+  __device__ __forceinline__ void read(int stage, int array, int k, int tid, int d, float* v) const {
+    Raw8<T> raw = zero_raw<T>();
+    if ((k * NT + tid) * 8 < d) {
+      raw.a = read16(slot(stage, array, k, 0));
+      if constexpr (kPiece == 32) raw.b = read16(slot(stage, array, k, 1));
+    }
+    unpack(raw, v);
+  }
+};
+__device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void ring_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// u (and its 8-bit form) of one row from h, whose pieces are in v; the thread's pre-gains in w.
+template <typename T, int NT, int VPT>
+__device__ __forceinline__ void finish_row(const NormP& p, int64_t row, int tid, const float* v,
+                                           const float* w, float r) {
+  const int d = p.features;
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) {
+    const int c = (k * NT + tid) * 8;
+    float u[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[j] = c < d ? w[8 * k + j] * (v[8 * k + j] * r) : 0.f;
+    if (c < d) store8(static_cast<T*>(p.u) + row * p.ldu + c, u);
+    if (p.q) keep8(p.q + row * p.ldq, p.scale + row * (p.ldq / 32), c, (int)p.ldq, u);
+  }
+}
+
+template <typename T, int NT, int VPT, int STAGES>
+__global__ void __launch_bounds__(cta_threads(NT), ctas_per_sm(NT)) k_norm_stream(const NormP p) {
+  constexpr int E = 8 * VPT, RPC = NT == 32 ? kWarpRows : 1;
+  extern __shared__ uint4 ring_smem[];
+  __shared__ float red[NT == 32 ? 1 : NT / 32];
+  const Ring<T, NT, VPT, 2> ring(ring_smem);
+  const int tid = NT == 32 ? threadIdx.x & 31 : threadIdx.x;
+  const int d = p.features;
+  const int64_t step = (int64_t)gridDim.x * RPC;
+  const int64_t first = (int64_t)blockIdx.x * RPC + (NT == 32 ? threadIdx.x >> 5 : 0);
+  auto fetch = [&](int64_t row, int stage) {
+    if (row < p.tokens) {
+      ring.fetch(stage, 0, static_cast<const T*>(p.x) + row * p.ldx, tid, d);
+      if (p.y) ring.fetch(stage, 1, static_cast<const T*>(p.y) + row * p.ldy, tid, d);
+    }
+    ring_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) fetch(first + i * step, i);
+  float w[E], c[E];
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) {
+    float a[8], b[8];
+    gains<NT, true>(p.pre, tid, k, d, w + 8 * k);
+    gains<NT, true>(p.post, tid, k, d, a);
+    gains<NT, true>(p.gate, tid, k, d, b);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c[8 * k + j] = a[j] * b[j];
+  }
+  int stage = 0;
+  for (int64_t row = first; row < p.tokens; row += step) {
+    ring_wait<STAGES - 2>();
+    float h[E];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) ring.read(stage, 0, k, tid, d, h + 8 * k);
+    float ss[1] = {0.f};
+    if (p.y) {
+      float y[E];
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) ring.read(stage, 1, k, tid, d, y + 8 * k);
+      float f = p.s;
+      if (p.post_norm) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) ss[0] = fmaf(y[e], y[e], ss[0]);
+        row_sum<NT, 1>(ss, red);
+        f *= rsqrtf(fmaf(ss[0], p.inv_d, p.eps));
+        ss[0] = 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) h[e] = fmaf(c[e], y[e] * f, h[e]);
+      if (p.h) store_row<T, NT, VPT, true>(static_cast<T*>(p.h) + row * p.ldh, tid, d, h);
+    }
+    // the slots read in the last round take the next row
+    fetch(row + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
+    if (++stage == STAGES) stage = 0;
+    if (!p.u) continue;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (column<NT, true>(tid, e) < d) ss[0] = fmaf(h[e], h[e], ss[0]);
+    row_sum<NT, 1>(ss, red);
+    finish_row<T, NT, VPT>(p, row, tid, h, w, rsqrtf(fmaf(ss[0], p.inv_d, p.eps)));
+  }
+  ring_wait<0>();
+}
+
+// This CTA's column sums; where a CTA holds several rows its warps add theirs in order.  The
+// parts' rows are padded to whole vectors.
+__host__ __device__ constexpr int64_t part_ld(int64_t d) { return (d + 7) / 8 * 8; }
+template <int NT, int VPT, bool AL>
+__device__ __forceinline__ void write_parts(const NormGradP& p, int tid, float* apre, float* apost) {
+  constexpr int E = 8 * VPT, RPC = NT == 32 ? kWarpRows : 1;
+  __shared__ float sum[NT == 32 ? 2 * E * 32 : 1];
+  const int d = p.features;
+  float* part = p.parts + blockIdx.x * 2 * part_ld(d);
+  if (NT == 32) {
+    for (int turn = 0; turn < RPC; ++turn) {
+      if ((threadIdx.x >> 5) == turn)
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          apre[e] += turn ? sum[e * 32 + tid] : 0.f;
+          apost[e] += turn ? sum[(E + e) * 32 + tid] : 0.f;
+          sum[e * 32 + tid] = apre[e];
+          sum[(E + e) * 32 + tid] = apost[e];
+        }
+      __syncthreads();
+    }
+    if ((threadIdx.x >> 5) != RPC - 1) return;
+  }
+  if (AL) {
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int c = (k * NT + tid) * 8;
+      if (c < d) {
+        store8(part + c, apre + 8 * k);
+        store8(part + part_ld(d) + c, apost + 8 * k);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int c = column<NT, AL>(tid, e);
+      if (c < d) {
+        part[c] = apre[e];
+        part[part_ld(d) + c] = apost[e];
+      }
+    }
+  }
+}
+
+template <typename T, int NT, int VPT, int STAGES>
+__global__ void __launch_bounds__(cta_threads(NT), ctas_per_sm(NT)) k_norm_grad_stream(const NormGradP p) {
+  constexpr int E = 8 * VPT, RPC = NT == 32 ? kWarpRows : 1;
+  extern __shared__ uint4 ring_smem[];
+  __shared__ float red[NT == 32 ? 1 : 3 * NT / 32];
+  enum { H, DU, DH, Y };
+  const Ring<T, NT, VPT, 4> ring(ring_smem);
+  const int tid = NT == 32 ? threadIdx.x & 31 : threadIdx.x;
+  const int d = p.features;
+  const int64_t step = (int64_t)gridDim.x * RPC;
+  const int64_t first = (int64_t)blockIdx.x * RPC + (NT == 32 ? threadIdx.x >> 5 : 0);
+  auto fetch = [&](int64_t row, int stage) {
+    if (row < p.tokens) {
+      if (p.du) {
+        ring.fetch(stage, H, static_cast<const T*>(p.h) + row * p.ldh, tid, d);
+        ring.fetch(stage, DU, static_cast<const T*>(p.du) + row * p.lddu, tid, d);
+      }
+      if (p.dh) ring.fetch(stage, DH, static_cast<const T*>(p.dh) + row * p.lddh, tid, d);
+      if (p.y) ring.fetch(stage, Y, static_cast<const T*>(p.y) + row * p.ldy, tid, d);
+    }
+    ring_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) fetch(first + i * step, i);
+  float w[E], c[E], apre[E], apost[E];
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) {
+    float a[8], b[8];
+    gains<NT, true>(p.pre, tid, k, d, w + 8 * k);
+    gains<NT, true>(p.post, tid, k, d, a);
+    gains<NT, true>(p.gate, tid, k, d, b);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c[8 * k + j] = p.s * a[j] * b[j];
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) apre[e] = apost[e] = 0.f;
+  int stage = 0;
+  for (int64_t row = first; row < p.tokens; row += step) {
+    ring_wait<STAGES - 2>();
+    // the slots read in the last round take the next row
+    fetch(row + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
+    float sum[3] = {0.f, 0.f, 0.f};
+    if (p.du)
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        float h[8], u[8];
+        ring.read(stage, H, k, tid, d, h);
+        ring.read(stage, DU, k, tid, d, u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          sum[0] = fmaf(h[j], h[j], sum[0]);
+          sum[1] = fmaf(w[8 * k + j] * u[j], h[j], sum[1]);
+        }
+      }
+    if (p.y && p.post_norm)
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        float y[8];
+        ring.read(stage, Y, k, tid, d, y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[2] = fmaf(y[j], y[j], sum[2]);
+      }
+    row_sum<NT, 3>(sum, red);
+    float g[E];
+    const float r = rsqrtf(fmaf(sum[0], p.inv_d, p.eps));
+    const float m1 = sum[1] * r * p.inv_d;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      float h[8], u[8];
+      if (p.dh) {
+        ring.read(stage, DH, k, tid, d, g + 8 * k);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[8 * k + j] = 0.f;
+      }
+      if (p.du) {
+        ring.read(stage, H, k, tid, d, h);
+        ring.read(stage, DU, k, tid, d, u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int e = 8 * k + j;
+          const float hn = h[j] * r;
+          apre[e] = fmaf(u[j], hn, apre[e]);
+          g[e] = fmaf(r, fmaf(-hn, m1, w[e] * u[j]), g[e]);
+        }
+      }
+    }
+    if (p.dx) store_row<T, NT, VPT, true>(static_cast<T*>(p.dx) + row * p.lddx, tid, d, g);
+    if (p.y) {
+      const float ry = p.post_norm ? rsqrtf(fmaf(sum[2], p.inv_d, p.eps)) : 1.f;
+      float dot[1] = {0.f};
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        float y[8];
+        ring.read(stage, Y, k, tid, d, y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int e = 8 * k + j;
+          const float yn = y[j] * ry;
+          apost[e] = fmaf(g[e], yn, apost[e]);
+          g[e] *= c[e];
+          dot[0] = fmaf(g[e], yn, dot[0]);
+        }
+      }
+      if (p.post_norm) {
+        row_sum<NT, 1>(dot, red);
+        const float m2 = dot[0] * p.inv_d;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+          float y[8];
+          ring.read(stage, Y, k, tid, d, y);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) g[8 * k + j] = ry * fmaf(-y[j] * ry, m2, g[8 * k + j]);
+        }
+      }
+      if (p.dy) store_row<T, NT, VPT, true>(static_cast<T*>(p.dy) + row * p.lddy, tid, d, g);
+    }
+    if (++stage == STAGES) stage = 0;
+  }
+  ring_wait<0>();
+  write_parts<NT, VPT, true>(p, tid, apre, apost);
+}
+
+// The form without a ring.  Rows of more than two pieces a thread keep the column sums in
+// shared memory (registers would spill), each thread its own columns'.
 template <typename T, int NT, int VPT, bool AL>
-__global__ void __launch_bounds__(NT == 32 ? 32 * kWarpRows : NT) k_norm_grad(const NormGradP p) {
+__global__ void __launch_bounds__(cta_threads(NT)) k_norm_grad(const NormGradP p) {
   constexpr int E = 8 * VPT;
   constexpr int RPC = NT == 32 ? kWarpRows : 1;
+  constexpr bool WIDE = VPT > 2;
+  extern __shared__ float wide[];  // [2][E][NT]
   __shared__ float red[NT == 32 ? 1 : 3 * NT / 32];
   const int tid = NT == 32 ? threadIdx.x & 31 : threadIdx.x;
   const int sub = NT == 32 ? threadIdx.x >> 5 : 0;
   const int d = p.features;
-  float apre[E], apost[E];
+  float apre[WIDE ? 1 : E], apost[WIDE ? 1 : E];
+  if (WIDE) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) apre[e] = apost[e] = 0.f;
+    for (int e = 0; e < 2 * E; ++e) wide[e * NT + tid] = 0.f;
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) apre[WIDE ? 0 : e] = apost[WIDE ? 0 : e] = 0.f;
+  }
+  auto add_pre = [&](int e, float a, float b) {
+    if (WIDE) wide[e * NT + tid] = fmaf(a, b, wide[e * NT + tid]);
+    else apre[WIDE ? 0 : e] = fmaf(a, b, apre[WIDE ? 0 : e]);
+  };
+  auto add_post = [&](int e, float a, float b) {
+    if (WIDE) wide[(E + e) * NT + tid] = fmaf(a, b, wide[(E + e) * NT + tid]);
+    else apost[WIDE ? 0 : e] = fmaf(a, b, apost[WIDE ? 0 : e]);
+  };
   for (int64_t row = (int64_t)blockIdx.x * RPC + sub; row < p.tokens; row += (int64_t)gridDim.x * RPC) {
     float h[E], g[E], w[E], y[E];  // w: du; g: dh, then the gradient of h
     float sum[3] = {0.f, 0.f, 0.f};
@@ -286,7 +613,7 @@ __global__ void __launch_bounds__(NT == 32 ? 32 * kWarpRows : NT) k_norm_grad(co
         for (int j = 0; j < 8; ++j) {
           const int e = 8 * k + j;
           const float hn = h[e] * r;
-          apre[e] = fmaf(w[e], hn, apre[e]);
+          add_pre(e, w[e], hn);
           g[e] = fmaf(r, fmaf(-hn, m1, a[j] * w[e]), g[e]);
         }
       }
@@ -304,7 +631,7 @@ __global__ void __launch_bounds__(NT == 32 ? 32 * kWarpRows : NT) k_norm_grad(co
       for (int j = 0; j < 8; ++j) {
         const int e = 8 * k + j;
         y[e] *= ry;
-        apost[e] = fmaf(g[e], y[e], apost[e]);
+        add_post(e, g[e], y[e]);
         g[e] *= p.s * a[j] * b[j];
         dot[0] = fmaf(g[e], y[e], dot[0]);
       }
@@ -317,20 +644,18 @@ __global__ void __launch_bounds__(NT == 32 ? 32 * kWarpRows : NT) k_norm_grad(co
     }
     if (p.dy) store_row<T, NT, VPT, AL>(static_cast<T*>(p.dy) + row * p.lddy, tid, d, g);
   }
-  // this CTA's column sums; in the warp-per-row form the warps add theirs in order
-  float* part = p.parts + (int64_t)blockIdx.x * 2 * d;
-  for (int turn = 0; turn < RPC; ++turn) {
-    if (sub == turn) {
+  if (WIDE) {
+    float* part = p.parts + blockIdx.x * 2 * part_ld(d);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int c = column<NT, AL>(tid, e);
-        if (c < d) {
-          part[c] = (turn ? part[c] : 0.f) + apre[e];
-          part[d + c] = (turn ? part[d + c] : 0.f) + apost[e];
-        }
+    for (int e = 0; e < E; ++e) {
+      const int c = column<NT, AL>(tid, e);
+      if (c < d) {
+        part[c] = wide[e * NT + tid];
+        part[part_ld(d) + c] = wide[(E + e) * NT + tid];
       }
     }
-    if (RPC > 1) __syncthreads();
+  } else {
+    write_parts<NT, WIDE ? 2 : VPT, AL>(p, tid, apre, apost);
   }
 }
 
@@ -343,18 +668,20 @@ struct GainP {
   int accumulate;
 };
 
-// Adds the CTAs' partial sums of 32 columns: eight warps take every eighth part, and the
-// eight sums are added in order.
-__global__ void __launch_bounds__(256) k_norm_gains(const GainP p) {
-  __shared__ float sh[2][8][32];
+// Adds the CTAs' partial sums of 32 columns: each warp takes every kGainWarps-th part, and the
+// warps' sums are added in order.
+constexpr int kGainWarps = 32;
+__global__ void __launch_bounds__(32 * kGainWarps) k_norm_gains(const GainP p) {
+  __shared__ float sh[2][kGainWarps][32];
   const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
   const int c = blockIdx.x * 32 + l;
   float a = 0.f, b = 0.f;
   if (c < p.features) {
-    for (int k = w; k < p.nparts; k += 8) {
-      const float* part = p.parts + (int64_t)k * 2 * p.features + c;
+#pragma unroll 4
+    for (int k = w; k < p.nparts; k += kGainWarps) {
+      const float* part = p.parts + k * 2 * part_ld(p.features) + c;
       a += part[0];
-      b += part[p.features];
+      b += part[part_ld(p.features)];
     }
   }
   sh[0][w][l] = a;
@@ -362,7 +689,8 @@ __global__ void __launch_bounds__(256) k_norm_gains(const GainP p) {
   __syncthreads();
   if (w != 0 || c >= p.features) return;
   a = b = 0.f;
-  for (int k = 0; k < 8; ++k) {
+#pragma unroll
+  for (int k = 0; k < kGainWarps; ++k) {
     a += sh[0][k][l];
     b += sh[1][k][l];
   }
@@ -372,43 +700,92 @@ __global__ void __launch_bounds__(256) k_norm_gains(const GainP p) {
   if (p.dgate) p.dgate[c] = (p.accumulate ? p.dgate[c] : 0.f) + p.s * post * b;
 }
 
-// Threads of a row and 8-element vectors of a thread, by the features: a warp up to 1024,
-// then the smallest CTA that holds the row in two vectors a thread, four at the widest.
+// Threads of a row and 8-element pieces of a thread, by the features: a warp up to 512, then
+// the smallest CTA that holds the row in two pieces a thread, four at the widest.
 template <typename F>
 void by_width(int64_t d, F f) {
   if (d <= 256) f(std::integral_constant<int, 32>(), std::integral_constant<int, 1>());
   else if (d <= 512) f(std::integral_constant<int, 32>(), std::integral_constant<int, 2>());
-  else if (d <= 1024) f(std::integral_constant<int, 32>(), std::integral_constant<int, 4>());
+  else if (d <= 1024) f(std::integral_constant<int, 64>(), std::integral_constant<int, 2>());
   else if (d <= 2048) f(std::integral_constant<int, 128>(), std::integral_constant<int, 2>());
   else if (d <= 4096) f(std::integral_constant<int, 256>(), std::integral_constant<int, 2>());
   else if (d <= 8192) f(std::integral_constant<int, 512>(), std::integral_constant<int, 2>());
   else f(std::integral_constant<int, 512>(), std::integral_constant<int, 4>());
 }
 
-template <typename T>
-void launch_norm(const NormP& p, bool al, cudaStream_t s) {
-  by_width(p.features, [&](auto nt, auto vpt) {
-    constexpr int NT = decltype(nt)::value, VPT = decltype(vpt)::value;
-    const unsigned grid = (unsigned)(NT == 32 ? (p.tokens + kWarpRows - 1) / kWarpRows : p.tokens);
-    const unsigned threads = NT == 32 ? 32 * kWarpRows : NT;
-    if (al) k_norm<T, NT, VPT, true><<<grid, threads, 0, s>>>(p);
-    else k_norm<T, NT, VPT, false><<<grid, threads, 0, s>>>(p);
-  });
+// CTAs that take all rows when each takes its share once, and a streaming grid's.
+int64_t row_ctas(int64_t tokens, int nt) { return nt == 32 ? (tokens + kWarpRows - 1) / kWarpRows : tokens; }
+int64_t stream_ctas(int nt) { return (int64_t)kSms * ctas_per_sm(nt); }
+
+cudaError_t allow_smem(const void* kernel, int bytes) {
+  return bytes <= 32 * 1024 ? cudaSuccess  // with the static part well inside the default limit
+                            : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+// Rows of the rings: three, two where three do not fit, none (the direct form) past that.
+// fp32 forward takes the direct form: a thread's piece is two 16-byte copies there, half a
+// sector each, and the stream of 8192 x 4096 ran at 133 us against 100 us.
+template <typename T, int NT, int VPT, int A>
+int ring_stages() {
+  if (sizeof(T) == 4 && A == 2) return 0;
+  constexpr int stage = Ring<T, NT, VPT, A>::kStage * ctas_per_sm(NT);
+  return VPT > 2 ? 0 : 3 * stage <= kSmemMost ? 3 : 2 * stage <= kSmemMost ? 2 : 0;
 }
 
 template <typename T>
-void launch_grad(const NormGradP& p, bool al, unsigned grid, cudaStream_t s) {
+cudaError_t launch_norm(const NormP& p, bool al, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
   by_width(p.features, [&](auto nt, auto vpt) {
     constexpr int NT = decltype(nt)::value, VPT = decltype(vpt)::value;
-    const unsigned threads = NT == 32 ? 32 * kWarpRows : NT;
-    if (al) k_norm_grad<T, NT, VPT, true><<<grid, threads, 0, s>>>(p);
-    else k_norm_grad<T, NT, VPT, false><<<grid, threads, 0, s>>>(p);
+    const int64_t rows = row_ctas(p.tokens, NT), fixed = stream_ctas(NT);
+    if constexpr (VPT <= 2) {
+      const int stages = ring_stages<T, NT, VPT, 2>();
+      if (al && stages > 0) {
+        const int bytes = stages * Ring<T, NT, VPT, 2>::kStage;
+        auto* kernel = stages == 3 ? k_norm_stream<T, NT, VPT, 3> : k_norm_stream<T, NT, VPT, 2>;
+        e = allow_smem((const void*)kernel, bytes);
+        if (e == cudaSuccess) kernel<<<(unsigned)std::min(rows, fixed), cta_threads(NT), bytes, s>>>(p);
+        return;
+      }
+    }
+    if (al) k_norm<T, NT, VPT, true><<<(unsigned)rows, cta_threads(NT), 0, s>>>(p);
+    else k_norm<T, NT, VPT, false><<<(unsigned)rows, cta_threads(NT), 0, s>>>(p);
   });
+  return e;
+}
+
+template <typename T>
+cudaError_t launch_grad(const NormGradP& p, bool al, unsigned grid, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  by_width(p.features, [&](auto nt, auto vpt) {
+    constexpr int NT = decltype(nt)::value, VPT = decltype(vpt)::value;
+    if constexpr (VPT <= 2) {
+      const int stages = ring_stages<T, NT, VPT, 4>();
+      if (al && stages > 0) {
+        const int bytes = stages * Ring<T, NT, VPT, 4>::kStage;
+        auto* kernel = stages == 3 ? k_norm_grad_stream<T, NT, VPT, 3> : k_norm_grad_stream<T, NT, VPT, 2>;
+        e = allow_smem((const void*)kernel, bytes);
+        if (e == cudaSuccess) kernel<<<grid, cta_threads(NT), bytes, s>>>(p);
+        return;
+      }
+    }
+    const int bytes = VPT > 2 ? 2 * 8 * VPT * NT * 4 : 0;
+    auto* kernel = al ? k_norm_grad<T, NT, VPT, true> : k_norm_grad<T, NT, VPT, false>;
+    e = allow_smem((const void*)kernel, bytes);
+    if (e == cudaSuccess) kernel<<<grid, cta_threads(NT), bytes, s>>>(p);
+  });
+  return e;
 }
 
 unsigned grad_grid(int64_t tokens, int64_t features) {
-  const int64_t rows = features <= 1024 ? (tokens + kWarpRows - 1) / kWarpRows : tokens;
-  return (unsigned)(rows < kParts ? rows : kParts);
+  int64_t grid = 0;
+  by_width(features, [&](auto nt, auto) {
+    constexpr int NT = decltype(nt)::value;
+    // one CTA an SM until each has eight rows: every CTA adds a row of partial sums
+    const int64_t rows = row_ctas(tokens, NT);
+    grid = std::min(rows, rows < 8 * kSms ? (int64_t)kSms : stream_ctas(NT));
+  });
+  return (unsigned)grid;
 }
 
 dion_status check_norm(int64_t tokens, int64_t features, int32_t dtype, float eps, float s) {
@@ -480,11 +857,13 @@ dion_status norm_impl(const dion_norm* a, void* stream) {
   p.tokens = a->tokens; p.features = (int)a->features; p.post_norm = a->post_norm != 0;
   p.eps = a->eps; p.s = a->residual_scale; p.inv_d = (float)(1.0 / (double)a->features);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
   switch (a->dtype) {
-    case DION_BF16: launch_norm<__nv_bfloat16>(p, al, s); break;
-    case DION_FP16: launch_norm<__half>(p, al, s); break;
-    default: launch_norm<float>(p, al, s);
+    case DION_BF16: e = launch_norm<__nv_bfloat16>(p, al, s); break;
+    case DION_FP16: e = launch_norm<__half>(p, al, s); break;
+    default: e = launch_norm<float>(p, al, s);
   }
+  if (e != cudaSuccess) return set_error(DION_ERR_CUDA, "k_norm: %s", cudaGetErrorString(e));
   return launch_status("k_norm");
 }
 
@@ -534,18 +913,20 @@ dion_status norm_grad_impl(const dion_norm_grad* a, void* ws, size_t ws_bytes, v
     p.ldh = a->ldh; p.ldy = a->ldy; p.lddu = a->lddu; p.lddh = a->lddh; p.lddx = a->lddx; p.lddy = a->lddy;
     p.tokens = a->tokens; p.features = (int)a->features; p.post_norm = a->post_norm != 0;
     p.eps = a->eps; p.s = a->residual_scale; p.inv_d = (float)(1.0 / (double)a->features);
+    cudaError_t e = cudaSuccess;
     switch (a->dtype) {
-      case DION_BF16: launch_grad<__nv_bfloat16>(p, al, grid, s); break;
-      case DION_FP16: launch_grad<__half>(p, al, grid, s); break;
-      default: launch_grad<float>(p, al, grid, s);
+      case DION_BF16: e = launch_grad<__nv_bfloat16>(p, al, grid, s); break;
+      case DION_FP16: e = launch_grad<__half>(p, al, grid, s); break;
+      default: e = launch_grad<float>(p, al, grid, s);
     }
+    if (e != cudaSuccess) return set_error(DION_ERR_CUDA, "k_norm_grad: %s", cudaGetErrorString(e));
     DION_TRY(launch_status("k_norm_grad"));
   }
   if (!a->dpre_gain && !a->dpost_gain && !a->dgate) return DION_OK;
   // no rows: the sums are zero (added to nothing, or written as zeros)
   const GainP gp{static_cast<const float*>(ws), (int)grid, (int)a->features, a->post_gain, a->gate,
                  a->dpre_gain, a->dpost_gain, a->dgate, a->residual_scale, a->accumulate != 0};
-  k_norm_gains<<<(unsigned)((a->features + 31) / 32), 256, 0, s>>>(gp);
+  k_norm_gains<<<(unsigned)((a->features + 31) / 32), 32 * kGainWarps, 0, s>>>(gp);
   return launch_status("k_norm_gains");
 }
 
@@ -560,7 +941,7 @@ dion_status dion_norm_forward(const dion_norm* args, void* stream) {
 
 size_t dion_norm_backward_workspace(int64_t tokens, int64_t features) {
   if (tokens < 1 || tokens > dion::kMaxTokens || features < 1 || features > dion::kMaxFeatures) return 0;
-  return (size_t)dion::grad_grid(tokens, features) * 2 * (size_t)features * sizeof(float);
+  return (size_t)dion::grad_grid(tokens, features) * 2 * (size_t)dion::part_ld(features) * sizeof(float);
 }
 
 dion_status dion_norm_backward(const dion_norm_grad* args, void* d_workspace, size_t workspace_bytes,

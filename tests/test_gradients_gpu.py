@@ -64,7 +64,10 @@ NORM_SHAPES = [(1, 1, 0, 0), (3, 7, 0, 0), (5, 64, 0, 0), (4, 256, 0, 0), (9, 26
                (2, 512, 8, 0), (7, 1000, 0, 0), (6, 1024, 0, 0), (3, 1023, 1, 0), (5, 1032, 0, 0),
                (4, 2048, 0, 0), (3, 2056, 24, 0), (2, 4096, 0, 0), (600, 4096, 0, 0),
                (2, 4097, 0, 0), (3, 8192, 0, 0), (2, 8200, 0, 0), (2, 16384, 0, 0),
-               (2, 12345, 0, 0), (4, 512, 0, 1), (3, 4096, 3, 5), (1300, 96, 0, 0)]
+               (2, 12345, 0, 0), (4, 512, 0, 1), (3, 4096, 3, 5), (1300, 96, 0, 0),
+               # batches that are streamed, ragged in rows and columns
+               (4801, 104, 0, 0), (5000, 264, 8, 0), (2500, 1016, 0, 0), (1201, 2048, 0, 0),
+               (607, 4088, 8, 0), (301, 8192, 0, 0), (301, 8200, 0, 0)]
 
 
 def _norm_inputs(t, d, pad, shift, dtype, seed):
