@@ -8,24 +8,32 @@
 // which is zeros (2^15 rows of 4096 take 0.54 GB).
 //
 // The gradient sorts the positions by id (a stable radix sort, so equal ids keep their
-// order), and the sorted list is cut into segments of kSeg positions.  A CTA adds up the
-// rows of each run of equal ids in its segment; a run inside one segment is written to the
-// table at once, the pieces of a longer one go to the workspace and a second kernel adds
-// them in order.  No floating-point atomics: results repeat bit for bit.
+// order; one CTA does it for a batch of up to kSmall positions, in shared memory), and the
+// sorted list is cut into segments of kSeg positions.  A CTA adds up the rows of each run of
+// equal ids in its segment; a run inside one segment is written to the table at once, the
+// pieces of a longer one go to the workspace and a last kernel adds them in order.  Beside
+// the segments' CTAs others write the zeros of the rows that no token met, so that every row
+// of the table is written once.  No floating-point atomics: results repeat bit for bit.
 #include "operator.h"
 #include "rows.cuh"
+
+#include <algorithm>
+#include <type_traits>
 
 namespace dion {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kSeg = 32;             // sorted positions per segment
-constexpr int kCols = 8 * kThreads;  // columns of a CTA in the sum over a segment
 constexpr int kDigit = 8;            // bits per pass of the sort
 constexpr int kBins = 1 << kDigit;
 constexpr int kKeys = 16;                   // keys per thread of a sort tile
 constexpr int kTile = kThreads * kKeys;     // keys per CTA
-constexpr int kJoinWarps = 8;
+constexpr int kSmall = 16384;               // positions that one CTA sorts
+constexpr int kSmallBits = 14;              // of a position below kSmall
+constexpr int kSmallVocab = 1 << (32 - kSmallBits);  // key and position share a word below it
+constexpr int kZeroRows = 1024;             // rows of a CTA that writes zeros, at most
+constexpr int kJoinGroups = 4;              // threads that share a column in the join
 
 // ---------------------------------------------------------------- lookup
 struct LookupP {
@@ -102,6 +110,7 @@ struct SortP {
   const uint32_t *key_in, *val_in;
   uint32_t *key_out, *val_out;
   uint32_t* hist;  // [kBins][tiles]: counts, then the exclusive sums over (bin, tile)
+  uint32_t* nspans;  // set to zero by the sort
   int64_t tokens, vocab;
   int tiles, shift, first;
 };
@@ -115,6 +124,7 @@ __device__ __forceinline__ uint32_t sort_key(const SortP& p, int64_t i) {
 __global__ void __launch_bounds__(kThreads) k_sort_count(const SortP p) {
   __shared__ uint32_t bins[kBins];
   bins[threadIdx.x] = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.nspans = 0;
   __syncthreads();
   const int64_t base = (int64_t)blockIdx.x * kTile;
 #pragma unroll 4
@@ -211,40 +221,111 @@ __global__ void __launch_bounds__(kThreads) k_sort_scatter(const SortP p) {
   }
 }
 
+// The whole sort in one CTA: a key and its position share a word, the position in the low
+// bits, 16 words a thread.  A pass ranks each word among its warp's (32 at a time, by the
+// lanes that hold the same digit), sums the warps' counts per digit, and exchanges the words
+// through shared memory.
+constexpr int kSmallThreads = 1024, kSmallWarps = 32, kSmallKeys = kSmall / kSmallThreads;
+__global__ void __launch_bounds__(kSmallThreads, 1) k_sort_small(const SortP p, int passes) {
+  extern __shared__ uint32_t small_smem[];
+  uint32_t* words = small_smem;                        // [kSmall]
+  uint32_t* bins = small_smem + kSmall;                // [warp][kBins]
+  __shared__ uint32_t sums[kBins / 32];
+  const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
+  const int n = (int)p.tokens;
+  if (threadIdx.x == 0) *p.nspans = 0;
+  uint32_t word[kSmallKeys], pos[kSmallKeys];
+#pragma unroll
+  for (int k = 0; k < kSmallKeys; ++k) {
+    const int i = w * 32 * kSmallKeys + k * 32 + l;
+    word[k] = i < n ? sort_key(p, i) << kSmallBits | (uint32_t)i : 0xffffffffu;
+  }
+  for (int pass = 0; pass < passes; ++pass) {
+    const int shift = kSmallBits + pass * kDigit;
+    uint32_t* mine = bins + w * kBins;
+    for (int i = l; i < kBins; i += 32) mine[i] = 0;
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < kSmallKeys; ++k) {
+      // words past the end stay behind all others: all ones, and stable among equals
+      const uint32_t dig = word[k] >> shift & (kBins - 1);
+      const uint32_t same = __match_any_sync(0xffffffffu, dig);
+      const uint32_t rank = __popc(same & ((1u << l) - 1));
+      const uint32_t before = mine[dig];
+      __syncwarp();
+      if (rank == 0) mine[dig] = before + __popc(same);
+      __syncwarp();
+      pos[k] = before + rank;
+    }
+    __syncthreads();
+    // thread d < kBins: exclusive sums of digit d over the warps, then over the digits
+    uint32_t total = 0, scan = 0;
+    if (threadIdx.x < kBins) {
+      for (int i = 0; i < kSmallWarps; ++i) {
+        const uint32_t c = bins[i * kBins + threadIdx.x];
+        bins[i * kBins + threadIdx.x] = total;
+        total += c;
+      }
+      scan = total;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, scan, o);
+        if (l >= o) scan += y;
+      }
+      if (l == 31) sums[w] = scan;
+    }
+    __syncthreads();
+    if (threadIdx.x < kBins) {
+      uint32_t at = scan - total;
+      for (int i = 0; i < w; ++i) at += sums[i];
+      for (int i = 0; i < kSmallWarps; ++i) bins[i * kBins + threadIdx.x] += at;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kSmallKeys; ++k) words[mine[word[k] >> shift & (kBins - 1)] + pos[k]] = word[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kSmallKeys; ++k) word[k] = words[w * 32 * kSmallKeys + k * 32 + l];
+    __syncthreads();
+  }
+#pragma unroll
+  for (int k = 0; k < kSmallKeys; ++k) {
+    const int i = w * 32 * kSmallKeys + k * 32 + l;
+    if (i < n) {
+      p.key_out[i] = word[k] >> kSmallBits;
+      p.val_out[i] = word[k] & (kSmall - 1);
+    }
+  }
+}
+
 // ---------------------------------------------------------------- gradient
 struct GradP {
   const uint32_t *key, *val;  // sorted ids and their positions
   const void* dout;
   float* dtable;
-  float* parts;  // [segments][2][features]: a run's piece that began earlier / goes on later
+  float* parts;     // [segments][2][features]: a run's piece that began earlier / goes on later
+  uint32_t* spans;  // segments in which a run starts that goes on past their end
+  uint32_t* nspans;
   int64_t ldo, ldt, tokens, vocab, features;
+  int64_t sum_ctas;  // CTAs that add up segments; those after them write zeros
+  int col_ctas;      // CTAs that share a segment's columns
+  int zero_rows;
+  int vec_table;     // rows of the table take 16-byte stores
   float scale;
   int accumulate;
 };
 
-__global__ void __launch_bounds__(kThreads) k_embed_zero(float* dtable, int64_t ldt, int64_t vocab,
-                                                         int64_t features, int vec) {
-  const int64_t step = vec ? 4 : 1;
-  const int64_t per_row = features / step, total = vocab * per_row;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * kThreads) {
-    const int64_t row = i / per_row;
-    float* p = dtable + row * ldt + (i - row * per_row) * step;
-    if (vec) *reinterpret_cast<float4*>(p) = make_float4(0.f, 0.f, 0.f, 0.f);
-    else *p = 0.f;
-  }
+// Column e of this thread's eight, in the group of 8 NT columns that starts at c0.
+template <int NT, bool AL>
+__device__ __forceinline__ int64_t grad_col(int64_t c0, int e) {
+  return c0 + (AL ? threadIdx.x * 8 + e : e * NT + threadIdx.x);
 }
 
-template <bool AL>
-__device__ __forceinline__ int64_t grad_col(int e) {
-  return (int64_t)blockIdx.y * kCols + (AL ? threadIdx.x * 8 + e : e * kThreads + threadIdx.x);
-}
-
-template <bool AL>
-__device__ __forceinline__ void grad_store(float* p, int64_t features, const float* v, float scale,
-                                           bool add) {
+template <int NT, bool AL>
+__device__ __forceinline__ void grad_store(float* p, int64_t c0, int64_t features, const float* v,
+                                           float scale, bool add) {
   if (AL) {
-    const int64_t c = grad_col<AL>(0);
+    const int64_t c = grad_col<NT, AL>(c0, 0);
     if (c >= features) return;
     float o[8];
 #pragma unroll
@@ -258,65 +339,114 @@ __device__ __forceinline__ void grad_store(float* p, int64_t features, const flo
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int64_t c = grad_col<AL>(e);
+      const int64_t c = grad_col<NT, AL>(c0, e);
       if (c < features) p[c] = v[e] * scale + (add ? p[c] : 0.f);
     }
   }
 }
 
-template <typename T, bool AL>
-__global__ void __launch_bounds__(kThreads) k_embed_sum(const GradP p) {
+// First sorted position whose key is >= k.
+__device__ __forceinline__ int64_t lower_bound(const uint32_t* key, int64_t n, uint32_t k) {
+  int64_t lo = 0, hi = n;
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) / 2;
+    if (key[mid] < k) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Zeros of the rows [first, first + zero_rows) that no token met.
+template <int NT>
+__device__ __forceinline__ void write_zeros(const GradP& p, int64_t first) {
+  __shared__ uint8_t met[kZeroRows];
+  __shared__ int64_t range[2];
+  const int rows = (int)min((int64_t)p.zero_rows, p.vocab - first);
+  for (int i = threadIdx.x; i < rows; i += NT) met[i] = 0;
+  if (threadIdx.x < 2) range[threadIdx.x] = lower_bound(p.key, p.tokens, (uint32_t)(first + (threadIdx.x ? rows : 0)));
+  __syncthreads();
+  for (int64_t i = range[0] + threadIdx.x; i < range[1]; i += NT) met[p.key[i] - first] = 1;
+  __syncthreads();
+  if (p.vec_table && p.features >= 4 * NT) {  // a row at a time
+    for (int r = 0; r < rows; ++r) {
+      if (met[r]) continue;
+      float4* to = reinterpret_cast<float4*>(p.dtable + (first + r) * p.ldt);
+      for (int64_t c = threadIdx.x; c < p.features / 4; c += NT) to[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    return;
+  }
+  const uint32_t step = p.vec_table ? 4 : 1, per_row = (uint32_t)(p.features / step);
+  const uint32_t total = rows * per_row;  // zero_rows * features < 2^31
+  for (uint32_t i = threadIdx.x; i < total; i += NT) {
+    const uint32_t r = i / per_row;
+    if (met[r]) continue;
+    float* to = p.dtable + (first + r) * p.ldt + (i - r * per_row) * step;
+    if (p.vec_table) *reinterpret_cast<float4*>(to) = make_float4(0.f, 0.f, 0.f, 0.f);
+    else *to = 0.f;
+  }
+}
+
+template <typename T, int NT, bool AL>
+__global__ void __launch_bounds__(NT) k_embed_sum(const GradP p) {
+  if (blockIdx.x >= p.sum_ctas) {
+    write_zeros<NT>(p, (blockIdx.x - p.sum_ctas) * p.zero_rows);
+    return;
+  }
   __shared__ uint32_t key[kSeg + 2], val[kSeg];  // key[0], key[n + 1]: the neighbours
-  const int64_t s0 = (int64_t)blockIdx.x * kSeg;
+  const int64_t seg = blockIdx.x / p.col_ctas;
+  const int64_t col0 = (blockIdx.x - seg * p.col_ctas) * (8 * NT);
+  const int64_t s0 = seg * kSeg;
   const int n = (int)min((int64_t)kSeg, p.tokens - s0);
   const uint32_t none = 0xffffffffu;
-  for (int i = threadIdx.x; i < n + 2; i += kThreads) {
+  for (int i = threadIdx.x; i < n + 2; i += NT) {
     const int64_t at = s0 + i - 1;
     key[i] = at >= 0 && at < p.tokens ? p.key[at] : none;
     if (i >= 1 && i <= n) val[i - 1] = p.val[at];
   }
   __syncthreads();
-  constexpr int U = 4;
+  constexpr int U = 8;
   float acc[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) acc[e] = 0.f;
   bool began = key[0] == key[1];  // the current run began in an earlier segment
   const T* dout = static_cast<const T*>(p.dout);
-  const int64_t c0 = grad_col<AL>(0);
+  const int64_t c0 = grad_col<NT, AL>(col0, 0);
   for (int i0 = 0; i0 < n; i0 += U) {
     if (key[i0 + 1] >= p.vocab) break;  // padding, sorted last
-    float v[U][8];
+    Raw8<T> raw[AL ? U : 1];
     if (AL) {
-      Raw8<T> raw[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        raw[u] = i0 + u < n && key[i0 + u + 1] < p.vocab && c0 < p.features
-                     ? load_raw(dout + val[i0 + u] * p.ldo + c0) : zero_raw<T>();
-#pragma unroll
-      for (int u = 0; u < U; ++u) unpack(raw[u], v[u]);
-    } else {
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int64_t c = grad_col<AL>(e);
-          v[u][e] = i0 + u < n && key[i0 + u + 1] < p.vocab && c < p.features
-                        ? to_float(dout[val[i0 + u] * p.ldo + c]) : 0.f;
-        }
+        raw[AL ? u : 0] = i0 + u < n && key[i0 + u + 1] < p.vocab && c0 < p.features
+                              ? load_raw(dout + val[i0 + u] * p.ldo + c0) : zero_raw<T>();
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u;
       if (i >= n || key[i + 1] >= p.vocab) break;
+      float v[8];
+      if (AL) {
+        unpack(raw[AL ? u : 0], v);
+      } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += v[u][e];
-      const bool last = i == n - 1;
+        for (int e = 0; e < 8; ++e) {
+          const int64_t c = grad_col<NT, AL>(col0, e);
+          v[e] = c < p.features ? to_float(dout[val[i] * p.ldo + c]) : 0.f;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] += v[e];
       const bool goes_on = key[i + 2] == key[i + 1];
-      if (goes_on && !last) continue;
-      float* parts = p.parts + (int64_t)blockIdx.x * 2 * p.features;
-      if (began) grad_store<AL>(parts, p.features, acc, 1.f, false);
-      else if (goes_on) grad_store<AL>(parts + p.features, p.features, acc, 1.f, false);
-      else grad_store<AL>(p.dtable + (int64_t)key[i + 1] * p.ldt, p.features, acc, p.scale, p.accumulate);
+      if (goes_on && i != n - 1) continue;
+      float* parts = p.parts + seg * 2 * p.features;
+      if (began) {
+        grad_store<NT, AL>(parts, col0, p.features, acc, 1.f, false);
+      } else if (goes_on) {
+        grad_store<NT, AL>(parts + p.features, col0, p.features, acc, 1.f, false);
+        if (threadIdx.x == 0 && col0 == 0) p.spans[atomicAdd(p.nspans, 1u)] = (uint32_t)seg;
+      } else {
+        grad_store<NT, AL>(p.dtable + (int64_t)key[i + 1] * p.ldt, col0, p.features, acc, p.scale, p.accumulate);
+      }
       began = false;
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc[e] = 0.f;
@@ -324,39 +454,43 @@ __global__ void __launch_bounds__(kThreads) k_embed_sum(const GradP p) {
   }
 }
 
-// Joins the pieces of the runs that cross segments: the segment where such a run starts
-// adds its pieces, each warp every kJoinWarps-th, and then the warps' sums, in order.
-__global__ void __launch_bounds__(32 * kJoinWarps) k_embed_join(const GradP p) {
-  __shared__ float sh[kJoinWarps][32];
-  const int64_t seg = blockIdx.x;
-  const int64_t end = min(p.tokens, (seg + 1) * kSeg);
-  if (end >= p.tokens) return;
-  const uint32_t k = p.key[end - 1];
-  if (k >= p.vocab || p.key[end] != k) return;                      // no run goes on
-  const int64_t s0 = seg * kSeg;
-  if (s0 > 0 && p.key[s0] == k && p.key[s0 - 1] == k) return;       // it began earlier
-  int64_t lo = end, hi = p.tokens;                                   // first position past the run
-  while (lo < hi) {
-    const int64_t mid = (lo + hi) / 2;
-    if (p.key[mid] == k) lo = mid + 1;
-    else hi = mid;
-  }
-  const int64_t last = (lo - 1) / kSeg;
-  const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
-  for (int64_t c0 = (int64_t)blockIdx.y * 32; c0 < p.features; c0 += (int64_t)gridDim.y * 32) {
-    const int64_t c = c0 + l;
+// Joins the pieces of the runs that cross segments.  The list's order varies from run to run,
+// a row's sum does not: kJoinGroups threads a column take every kJoinGroups-th piece each, and
+// their sums are added in order.
+constexpr int kJoinCols = 128;
+__global__ void __launch_bounds__(kJoinCols * kJoinGroups) k_embed_join(const GradP p) {
+  __shared__ float sh[kJoinGroups][kJoinCols];
+  const int64_t blocks = (p.features + kJoinCols - 1) / kJoinCols;
+  const int64_t items = *p.nspans * blocks;
+  const int g = threadIdx.x / kJoinCols, l = threadIdx.x % kJoinCols, lane = threadIdx.x & 31;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int64_t seg = p.spans[item / blocks];
+    const int64_t end = (seg + 1) * kSeg;  // inside the list: the run goes on there
+    const uint32_t k = p.key[end];
+    // the run's last segment: 32 probes of the sorted list at a time
+    int64_t lo = end, hi = p.tokens;  // key[lo] == k; past hi it is not
+    while (hi - lo > 1) {
+      const int64_t step = (hi - lo + 32) / 33;
+      const int64_t at = lo + step * (lane + 1);
+      const uint32_t in = __ballot_sync(0xffffffffu, at < hi && p.key[at < hi ? at : lo] == k);
+      const int c = __popc(in);
+      hi = min(hi, lo + step * (c + 1));
+      lo += step * c;
+    }
+    const int64_t last = lo / kSeg;
+    const int64_t c = (item % blocks) * kJoinCols + l;
     float a = 0.f;
     if (c < p.features) {
-      if (w == 0) a = p.parts[(2 * seg + 1) * p.features + c];
+      if (g == 0) a = p.parts[(2 * seg + 1) * p.features + c];
 #pragma unroll 4
-      for (int64_t s = seg + 1 + w; s <= last; s += kJoinWarps) a += p.parts[2 * s * p.features + c];
+      for (int64_t s = seg + 1 + g; s <= last; s += kJoinGroups) a += p.parts[2 * s * p.features + c];
     }
-    sh[w][l] = a;
+    sh[g][l] = a;
     __syncthreads();
-    if (w == 0 && c < p.features) {
+    if (g == 0 && c < p.features) {
       a = 0.f;
 #pragma unroll
-      for (int i = 0; i < kJoinWarps; ++i) a += sh[i][l];
+      for (int i = 0; i < kJoinGroups; ++i) a += sh[i][l];
       float* to = p.dtable + (int64_t)k * p.ldt + c;
       *to = a * p.scale + (p.accumulate ? *to : 0.f);
     }
@@ -364,10 +498,20 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_embed_join(const GradP p) {
   }
 }
 
+__global__ void __launch_bounds__(kThreads) k_embed_zero(float* dtable, int64_t ldt, int64_t vocab,
+                                                         int64_t features) {
+  const int64_t total = vocab * features;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * kThreads) {
+    const int64_t row = i / features;
+    dtable[row * ldt + i - row * features] = 0.f;
+  }
+}
+
 // ---------------------------------------------------------------- host
 struct GradLayout {
   int64_t tiles, segs;
-  size_t key[2], val[2], hist, parts, bytes;
+  size_t key[2], val[2], hist, spans, parts, bytes;
 };
 
 GradLayout grad_layout(int64_t tokens, int64_t features) {
@@ -385,6 +529,7 @@ GradLayout grad_layout(int64_t tokens, int64_t features) {
     g.val[i] = take((size_t)tokens * 4);
   }
   g.hist = take((size_t)g.tiles * kBins * 4);
+  g.spans = take((size_t)(g.segs + 1) * 4);  // the count first
   g.parts = take((size_t)g.segs * 2 * (size_t)features * 4);
   g.bytes = at;
   return g;
@@ -450,10 +595,21 @@ dion_status lookup_impl(const dion_embed* a, void* stream) {
   return launch_status("k_embed_lookup");
 }
 
+// Threads of a segment's CTA: a warp's worth of 8 columns each up to 256 columns, at most 256.
 template <typename T>
-void launch_sum(const GradP& p, bool al, dim3 grid, cudaStream_t s) {
-  if (al) k_embed_sum<T, true><<<grid, kThreads, 0, s>>>(p);
-  else k_embed_sum<T, false><<<grid, kThreads, 0, s>>>(p);
+void launch_sum(GradP p, bool al, int64_t segs, cudaStream_t s) {
+  auto go = [&](auto nt) {
+    constexpr int NT = decltype(nt)::value;
+    p.col_ctas = (int)((p.features + 8 * NT - 1) / (8 * NT));
+    p.sum_ctas = segs * p.col_ctas;
+    const int64_t grid = p.sum_ctas + (p.accumulate ? 0 : (p.vocab + p.zero_rows - 1) / p.zero_rows);
+    if (al) k_embed_sum<T, NT, true><<<(unsigned)grid, NT, 0, s>>>(p);
+    else k_embed_sum<T, NT, false><<<(unsigned)grid, NT, 0, s>>>(p);
+  };
+  if (p.features <= 256) go(std::integral_constant<int, 32>());
+  else if (p.features <= 512) go(std::integral_constant<int, 64>());
+  else if (p.features <= 1024) go(std::integral_constant<int, 128>());
+  else go(std::integral_constant<int, 256>());
 }
 
 dion_status embed_grad_impl(const dion_embed_grad* a, void* ws, size_t ws_bytes, void* stream) {
@@ -473,12 +629,11 @@ dion_status embed_grad_impl(const dion_embed_grad* a, void* ws, size_t ws_bytes,
   int sms = 0;
   DION_TRY(check_sm100(&sms));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const bool vec_table = a->features % 4 == 0 && rows_aligned16(a->dtable, a->ldt, 4);
-  if (!a->accumulate) {
-    k_embed_zero<<<(unsigned)(sms * 8), kThreads, 0, s>>>(a->dtable, a->ldt, a->vocab, a->features, vec_table);
-    DION_TRY(launch_status("k_embed_zero"));
+  if (a->tokens == 0) {
+    if (a->accumulate) return DION_OK;
+    k_embed_zero<<<(unsigned)(sms * 8), kThreads, 0, s>>>(a->dtable, a->ldt, a->vocab, a->features);
+    return launch_status("k_embed_zero");
   }
-  if (a->tokens == 0) return DION_OK;
   char* base = static_cast<char*>(ws);
   uint32_t* key[2] = {reinterpret_cast<uint32_t*>(base + g.key[0]), reinterpret_cast<uint32_t*>(base + g.key[1])};
   uint32_t* val[2] = {reinterpret_cast<uint32_t*>(base + g.val[0]), reinterpret_cast<uint32_t*>(base + g.val[1])};
@@ -486,45 +641,62 @@ dion_status embed_grad_impl(const dion_embed_grad* a, void* ws, size_t ws_bytes,
   sp.ids = a->ids;
   sp.id64 = a->id_bytes == 8;
   sp.hist = reinterpret_cast<uint32_t*>(base + g.hist);
+  sp.nspans = reinterpret_cast<uint32_t*>(base + g.spans);
   sp.tokens = a->tokens;
   sp.vocab = a->vocab;
   sp.tiles = (int)g.tiles;
   int bits = 0;  // of the largest key, vocab (the padding's)
   while (bits < 32 && (a->vocab >> bits) != 0) ++bits;
+  const int passes = (bits + kDigit - 1) / kDigit;
   int at = 0;
-  for (int shift = 0; shift < bits; shift += kDigit, at ^= 1) {
-    sp.first = shift == 0;
-    sp.shift = shift;
-    sp.key_in = key[at ^ 1];
-    sp.val_in = val[at ^ 1];
-    sp.key_out = key[at];
-    sp.val_out = val[at];
-    k_sort_count<<<(unsigned)g.tiles, kThreads, 0, s>>>(sp);
-    k_sort_scan<<<1, 1024, 0, s>>>(sp.hist, (int64_t)kBins * g.tiles);
-    k_sort_scatter<<<(unsigned)g.tiles, kThreads, 0, s>>>(sp);
-    DION_TRY(launch_status("the sort of the tokens"));
+  if (a->tokens <= kSmall && a->vocab < kSmallVocab) {
+    constexpr int bytes = (kSmall + kSmallWarps * kBins) * 4;
+    const cudaError_t e = cudaFuncSetAttribute(k_sort_small, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return set_error(DION_ERR_CUDA, "k_sort_small: %s", cudaGetErrorString(e));
+    sp.first = 1;
+    sp.key_out = key[0];
+    sp.val_out = val[0];
+    k_sort_small<<<1, kSmallThreads, bytes, s>>>(sp, passes);
+    DION_TRY(launch_status("k_sort_small"));
+  } else {
+    for (int pass = 0; pass < passes; ++pass, at ^= 1) {
+      sp.first = pass == 0;
+      sp.shift = pass * kDigit;
+      sp.key_in = key[at ^ 1];
+      sp.val_in = val[at ^ 1];
+      sp.key_out = key[at];
+      sp.val_out = val[at];
+      k_sort_count<<<(unsigned)g.tiles, kThreads, 0, s>>>(sp);
+      k_sort_scan<<<1, 1024, 0, s>>>(sp.hist, (int64_t)kBins * g.tiles);
+      k_sort_scatter<<<(unsigned)g.tiles, kThreads, 0, s>>>(sp);
+      DION_TRY(launch_status("the sort of the tokens"));
+    }
+    at ^= 1;
   }
   GradP p{};
-  p.key = key[at ^ 1];
-  p.val = val[at ^ 1];
+  p.key = key[at];
+  p.val = val[at];
   p.dout = a->dout;
   p.dtable = a->dtable;
   p.parts = reinterpret_cast<float*>(base + g.parts);
+  p.nspans = sp.nspans;
+  p.spans = sp.nspans + 1;
   p.ldo = a->ldo; p.ldt = a->ldt;
   p.tokens = a->tokens; p.vocab = a->vocab; p.features = a->features;
   p.scale = a->scale;
   p.accumulate = a->accumulate != 0;
-  const bool al = a->features % 8 == 0 && vec_table && rows_aligned16(a->dout, a->ldo, es);
-  const dim3 grid((unsigned)g.segs, (unsigned)((a->features + kCols - 1) / kCols));
+  p.vec_table = a->features % 4 == 0 && rows_aligned16(a->dtable, a->ldt, 4);
+  // 128 KB of zeros to a CTA: enough to pay for finding its rows in the list
+  p.zero_rows = (int)std::max<int64_t>(1, std::min<int64_t>(kZeroRows, (128 << 10) / (4 * a->features)));
+  const bool al = a->features % 8 == 0 && p.vec_table && rows_aligned16(a->dout, a->ldo, es);
   switch (a->dtype) {
-    case DION_BF16: launch_sum<__nv_bfloat16>(p, al, grid, s); break;
-    case DION_FP16: launch_sum<__half>(p, al, grid, s); break;
-    default: launch_sum<float>(p, al, grid, s);
+    case DION_BF16: launch_sum<__nv_bfloat16>(p, al, g.segs, s); break;
+    case DION_FP16: launch_sum<__half>(p, al, g.segs, s); break;
+    default: launch_sum<float>(p, al, g.segs, s);
   }
   DION_TRY(launch_status("k_embed_sum"));
   if (g.segs > 1) {
-    const int64_t cols = (a->features + 31) / 32;
-    k_embed_join<<<dim3((unsigned)g.segs, (unsigned)(cols < 128 ? cols : 128)), 32 * kJoinWarps, 0, s>>>(p);
+    k_embed_join<<<(unsigned)(sms * 4), kJoinCols * kJoinGroups, 0, s>>>(p);
     DION_TRY(launch_status("k_embed_join"));
   }
   return DION_OK;

@@ -668,29 +668,38 @@ struct GainP {
   int accumulate;
 };
 
-// Adds the CTAs' partial sums of 32 columns: each warp takes every kGainWarps-th part, and the
-// warps' sums are added in order.
-constexpr int kGainWarps = 32;
-__global__ void __launch_bounds__(32 * kGainWarps) k_norm_gains(const GainP p) {
-  __shared__ float sh[2][kGainWarps][32];
+// Adds the CTAs' partial sums of COLS columns: the threads that share a column take turns over
+// the parts, and their sums are added in a fixed tree.  32 columns a CTA read whole lines; below
+// 4096 features 8 (a sector) leave more CTAs (16384 x 1024: 7 us, with 32 columns 10 us).
+constexpr int kGainThreads = 1024;
+template <int COLS>
+__global__ void __launch_bounds__(kGainThreads) k_norm_gains(const GainP p) {
+  __shared__ float sh[2][kGainThreads / 32][COLS];
   const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
-  const int c = blockIdx.x * 32 + l;
+  const int c = blockIdx.x * COLS + l % COLS;
   float a = 0.f, b = 0.f;
   if (c < p.features) {
 #pragma unroll 4
-    for (int k = w; k < p.nparts; k += kGainWarps) {
+    for (int k = threadIdx.x / COLS; k < p.nparts; k += kGainThreads / COLS) {
       const float* part = p.parts + k * 2 * part_ld(p.features) + c;
       a += part[0];
       b += part[part_ld(p.features)];
     }
   }
-  sh[0][w][l] = a;
-  sh[1][w][l] = b;
+#pragma unroll
+  for (int o = COLS; o < 32; o <<= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+  if (l < COLS) {
+    sh[0][w][l] = a;
+    sh[1][w][l] = b;
+  }
   __syncthreads();
-  if (w != 0 || c >= p.features) return;
+  if (threadIdx.x >= COLS || c >= p.features) return;
   a = b = 0.f;
 #pragma unroll
-  for (int k = 0; k < kGainWarps; ++k) {
+  for (int k = 0; k < kGainThreads / 32; ++k) {
     a += sh[0][k][l];
     b += sh[1][k][l];
   }
@@ -926,7 +935,8 @@ dion_status norm_grad_impl(const dion_norm_grad* a, void* ws, size_t ws_bytes, v
   // no rows: the sums are zero (added to nothing, or written as zeros)
   const GainP gp{static_cast<const float*>(ws), (int)grid, (int)a->features, a->post_gain, a->gate,
                  a->dpre_gain, a->dpost_gain, a->dgate, a->residual_scale, a->accumulate != 0};
-  k_norm_gains<<<(unsigned)((a->features + 31) / 32), 32 * kGainWarps, 0, s>>>(gp);
+  if (a->features >= 4096) k_norm_gains<32><<<(unsigned)((a->features + 31) / 32), kGainThreads, 0, s>>>(gp);
+  else k_norm_gains<8><<<(unsigned)((a->features + 7) / 8), kGainThreads, 0, s>>>(gp);
   return launch_status("k_norm_gains");
 }
 

@@ -430,7 +430,9 @@ def _ids(kind, t, v, seed):
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("kind", ["uniform", "one", "none", "few", "cycle"])
 @pytest.mark.parametrize("t,v,d,pad", [(1, 1, 8, 0), (31, 5, 24, 0), (33, 300, 40, 8), (64, 2, 7, 0),
-                                       (1000, 70000, 16, 0), (5000, 257, 130, 2), (9001, 40, 2064, 0)])
+                                       (1000, 70000, 16, 0), (5000, 257, 130, 2), (9001, 40, 2064, 0),
+                                       (16384, 255, 520, 0), (16385, 3000, 24, 0), (500, 300000, 8, 0),
+                                       (130, 262143, 8, 0), (70, 1030, 1032, 0)])
 def test_embed_grad(t, v, d, pad, kind, dtype):
     ids = _ids(kind, t, v, 3)
     dout = Rows(t, d, DT[dtype], pad, 0, fill=True, seed=4)
