@@ -8,7 +8,7 @@
 // which is zeros (2^15 rows of 4096 take 0.54 GB).
 //
 // The gradient sorts the positions by id (a stable radix sort, so equal ids keep their
-// order; one CTA does it for a batch of up to kSmall positions, in shared memory), and the
+// order; one cluster does it for a batch of up to kClusterMost positions), and the
 // sorted list is cut into segments of kSeg positions.  A CTA adds up the rows of each run of
 // equal ids in its segment; a run inside one segment is written to the table at once, the
 // pieces of a longer one go to the workspace and a last kernel adds them in order.  Beside
@@ -27,11 +27,8 @@ constexpr int kThreads = 256;
 constexpr int kSeg = 32;             // sorted positions per segment
 constexpr int kDigit = 8;            // bits per pass of the sort
 constexpr int kBins = 1 << kDigit;
-constexpr int kKeys = 16;                   // keys per thread of a sort tile
+constexpr int kKeys = 8;                    // keys per thread of a sort tile
 constexpr int kTile = kThreads * kKeys;     // keys per CTA
-constexpr int kSmall = 16384;               // positions that one CTA sorts
-constexpr int kSmallBits = 14;              // of a position below kSmall
-constexpr int kSmallVocab = 1 << (32 - kSmallBits);  // key and position share a word below it
 constexpr int kZeroRows = 1024;             // rows of a CTA that writes zeros, at most
 constexpr int kJoinGroups = 4;              // threads that share a column in the join
 
@@ -136,15 +133,19 @@ __global__ void __launch_bounds__(kThreads) k_sort_count(const SortP p) {
   p.hist[(int64_t)threadIdx.x * p.tiles + blockIdx.x] = bins[threadIdx.x];
 }
 
-// Exclusive sums over n counts in place, one CTA.
+// Exclusive sums over n counts in place (n a multiple of 8), one CTA, eight counts a thread.
 __global__ void __launch_bounds__(1024) k_sort_scan(uint32_t* hist, int64_t n) {
   __shared__ uint32_t warp_sum[32];
-  __shared__ uint32_t carry;
   const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
-  if (threadIdx.x == 0) carry = 0;
-  for (int64_t base = 0; base < n; base += 1024) {
-    const int64_t i = base + threadIdx.x;
-    const uint32_t v = i < n ? hist[i] : 0;
+  uint32_t carry = 0;
+  for (int64_t base = 0; base < n; base += 8 * 1024) {
+    const int64_t i = base + threadIdx.x * 8;
+    uint4 a = make_uint4(0, 0, 0, 0), b = a;
+    if (i < n) {
+      a = *reinterpret_cast<const uint4*>(hist + i);
+      b = *reinterpret_cast<const uint4*>(hist + i + 4);
+    }
+    const uint32_t v = a.x + a.y + a.z + a.w + b.x + b.y + b.z + b.w;
     uint32_t x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -153,20 +154,25 @@ __global__ void __launch_bounds__(1024) k_sort_scan(uint32_t* hist, int64_t n) {
     }
     if (l == 31) warp_sum[w] = x;
     __syncthreads();
-    if (w == 0) {
-      uint32_t t = warp_sum[l];
+    uint32_t t = warp_sum[l];  // every warp sums the warps' totals for itself
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, t, o);
-        if (l >= o) t += y;
-      }
-      warp_sum[l] = t;
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, t, o);
+      if (l >= o) t += y;
     }
-    __syncthreads();
-    const uint32_t before = carry + (w ? warp_sum[w - 1] : 0u) + x - v;
-    if (i < n) hist[i] = before;
-    __syncthreads();
-    if (threadIdx.x == 0) carry += warp_sum[31];
+    uint32_t at = carry + x - v + (w ? __shfl_sync(0xffffffffu, t, w - 1) : 0u);
+    carry += __shfl_sync(0xffffffffu, t, 31);
+    if (i < n) {
+      uint32_t c[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t own = c[k];
+        c[k] = at;
+        at += own;
+      }
+      *reinterpret_cast<uint4*>(hist + i) = make_uint4(c[0], c[1], c[2], c[3]);
+      *reinterpret_cast<uint4*>(hist + i + 4) = make_uint4(c[4], c[5], c[6], c[7]);
+    }
     __syncthreads();
   }
 }
@@ -221,52 +227,86 @@ __global__ void __launch_bounds__(kThreads) k_sort_scatter(const SortP p) {
   }
 }
 
-// The whole sort in one CTA: a key and its position share a word, the position in the low
-// bits, 16 words a thread.  A pass ranks each word among its warp's (32 at a time, by the
-// lanes that hold the same digit), sums the warps' counts per digit, and exchanges the words
-// through shared memory.
-constexpr int kSmallThreads = 1024, kSmallWarps = 32, kSmallKeys = kSmall / kSmallThreads;
-__global__ void __launch_bounds__(kSmallThreads, 1) k_sort_small(const SortP p, int passes) {
-  extern __shared__ uint32_t small_smem[];
-  uint32_t* words = small_smem;                        // [kSmall]
-  uint32_t* bins = small_smem + kSmall;                // [warp][kBins]
+// The whole sort in one cluster, for batches whose key and position fit one word (position in
+// the low bits).  CTA c holds words [c share, (c + 1) share), a warp 32 rounds of them; a pass
+// ranks each word among its warp's (32 at a time, by the lanes that hold the same digit), sums
+// the counts per digit over the warps and, through distributed shared memory, over the CTAs,
+// and sends each word to its place in whichever CTA holds it.  Ranking is what takes the time
+// (a __match_any_sync every 70 cycles or so on an SM), hence the eight SMs: in one CTA the sort
+// of 16384 positions took 40 us, with per-thread counters in place of the match 50 us.
+constexpr int kClusterCtas = 8, kClusterThreads = 512, kClusterKeys = 8;
+constexpr int64_t kClusterMost = (int64_t)kClusterCtas * kClusterThreads * kClusterKeys;
+
+__device__ __forceinline__ void sort_cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cta_address(const void* p, uint32_t cta) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(r) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(cta));
+  return r;
+}
+
+__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterThreads, 1)
+    k_sort_cluster(const SortP p, int passes, int pos_bits, int rounds) {
+  constexpr int W = kClusterThreads / 32;
+  __shared__ uint32_t words[2][kClusterThreads * kClusterKeys];
+  __shared__ uint16_t bins[W][kBins];  // places stay below 2^16
+  __shared__ uint32_t total[kBins];   // of this CTA, per digit
   __shared__ uint32_t sums[kBins / 32];
   const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
-  const int n = (int)p.tokens;
-  if (threadIdx.x == 0) *p.nspans = 0;
-  uint32_t word[kSmallKeys], pos[kSmallKeys];
+  const uint32_t cta = blockIdx.x;    // one cluster: the rank
+  const uint32_t share = (uint32_t)rounds * kClusterThreads;
+  const int first = w * 32 * rounds + l;
+  if (cta == 0 && threadIdx.x == 0) *p.nspans = 0;
 #pragma unroll
-  for (int k = 0; k < kSmallKeys; ++k) {
-    const int i = w * 32 * kSmallKeys + k * 32 + l;
-    word[k] = i < n ? sort_key(p, i) << kSmallBits | (uint32_t)i : 0xffffffffu;
+  for (int k = 0; k < kClusterKeys; ++k) {
+    if (k >= rounds) break;
+    const int64_t i = (int64_t)cta * share + first + k * 32;
+    // words past the end stay behind all others: all ones, and last among equals
+    words[0][first + k * 32] = i < p.tokens ? sort_key(p, i) << pos_bits | (uint32_t)i : 0xffffffffu;
   }
+  __syncwarp();
   for (int pass = 0; pass < passes; ++pass) {
-    const int shift = kSmallBits + pass * kDigit;
-    uint32_t* mine = bins + w * kBins;
-    for (int i = l; i < kBins; i += 32) mine[i] = 0;
+    const int shift = pos_bits + pass * kDigit;
+    for (int i = l; i < kBins; i += 32) bins[w][i] = 0;
     __syncwarp();
+    uint32_t word[kClusterKeys], pos[kClusterKeys];
 #pragma unroll
-    for (int k = 0; k < kSmallKeys; ++k) {
-      // words past the end stay behind all others: all ones, and stable among equals
+    for (int k = 0; k < kClusterKeys; ++k) {
+      if (k >= rounds) break;
+      word[k] = words[pass & 1][first + k * 32];
       const uint32_t dig = word[k] >> shift & (kBins - 1);
       const uint32_t same = __match_any_sync(0xffffffffu, dig);
       const uint32_t rank = __popc(same & ((1u << l) - 1));
-      const uint32_t before = mine[dig];
+      const uint32_t before = bins[w][dig];
       __syncwarp();
-      if (rank == 0) mine[dig] = before + __popc(same);
+      if (rank == 0) bins[w][dig] = (uint16_t)(before + __popc(same));
       __syncwarp();
       pos[k] = before + rank;
     }
     __syncthreads();
-    // thread d < kBins: exclusive sums of digit d over the warps, then over the digits
-    uint32_t total = 0, scan = 0;
     if (threadIdx.x < kBins) {
-      for (int i = 0; i < kSmallWarps; ++i) {
-        const uint32_t c = bins[i * kBins + threadIdx.x];
-        bins[i * kBins + threadIdx.x] = total;
-        total += c;
+      uint32_t at = 0;
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        const uint32_t c = bins[i][threadIdx.x];
+        bins[i][threadIdx.x] = (uint16_t)at;
+        at += c;
       }
-      scan = total;
+      total[threadIdx.x] = at;
+    }
+    sort_cluster_sync();
+    uint32_t all = 0, before = 0, scan = 0;  // of this digit: over the CTAs, in the earlier ones
+    if (threadIdx.x < kBins) {
+#pragma unroll
+      for (uint32_t c = 0; c < kClusterCtas; ++c) {
+        uint32_t v;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cta_address(&total[threadIdx.x], c)));
+        all += v;
+        before += c < cta ? v : 0;
+      }
+      scan = all;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const uint32_t y = __shfl_up_sync(0xffffffffu, scan, o);
@@ -276,24 +316,30 @@ __global__ void __launch_bounds__(kSmallThreads, 1) k_sort_small(const SortP p, 
     }
     __syncthreads();
     if (threadIdx.x < kBins) {
-      uint32_t at = scan - total;
+      uint32_t at = before + scan - all;
       for (int i = 0; i < w; ++i) at += sums[i];
-      for (int i = 0; i < kSmallWarps; ++i) bins[i * kBins + threadIdx.x] += at;
+#pragma unroll
+      for (int i = 0; i < W; ++i) bins[i][threadIdx.x] = (uint16_t)(bins[i][threadIdx.x] + at);
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kSmallKeys; ++k) words[mine[word[k] >> shift & (kBins - 1)] + pos[k]] = word[k];
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kSmallKeys; ++k) word[k] = words[w * 32 * kSmallKeys + k * 32 + l];
-    __syncthreads();
+    for (int k = 0; k < kClusterKeys; ++k) {
+      if (k >= rounds) break;
+      const uint32_t to = bins[w][word[k] >> shift & (kBins - 1)] + pos[k], owner = to / share;
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cta_address(&words[(pass & 1) ^ 1][to - owner * share], owner)),
+                   "r"(word[k])
+                   : "memory");
+    }
+    sort_cluster_sync();  // every word has arrived, and no CTA is read or written after the last
   }
 #pragma unroll
-  for (int k = 0; k < kSmallKeys; ++k) {
-    const int i = w * 32 * kSmallKeys + k * 32 + l;
-    if (i < n) {
-      p.key_out[i] = word[k] >> kSmallBits;
-      p.val_out[i] = word[k] & (kSmall - 1);
+  for (int k = 0; k < kClusterKeys; ++k) {
+    if (k >= rounds) break;
+    const int64_t i = (int64_t)cta * share + first + k * 32;
+    if (i < p.tokens) {
+      const uint32_t word = words[passes & 1][first + k * 32];
+      p.key_out[i] = word >> pos_bits;
+      p.val_out[i] = word & ((1u << pos_bits) - 1);
     }
   }
 }
@@ -456,43 +502,60 @@ __global__ void __launch_bounds__(NT) k_embed_sum(const GradP p) {
 
 // Joins the pieces of the runs that cross segments.  The list's order varies from run to run,
 // a row's sum does not: kJoinGroups threads a column take every kJoinGroups-th piece each, and
-// their sums are added in order.
-constexpr int kJoinCols = 128;
+// their sums are added in order.  V4: four columns a thread.
+constexpr int kJoinCols = 128;  // threads over the columns
+template <bool V4>
 __global__ void __launch_bounds__(kJoinCols * kJoinGroups) k_embed_join(const GradP p) {
-  __shared__ float sh[kJoinGroups][kJoinCols];
-  const int64_t blocks = (p.features + kJoinCols - 1) / kJoinCols;
+  constexpr int V = V4 ? 4 : 1;
+  __shared__ float sh[kJoinGroups][kJoinCols * V];
+  const int64_t blocks = (p.features + kJoinCols * V - 1) / (kJoinCols * V);
   const int64_t items = *p.nspans * blocks;
   const int g = threadIdx.x / kJoinCols, l = threadIdx.x % kJoinCols, lane = threadIdx.x & 31;
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
     const int64_t seg = p.spans[item / blocks];
-    const int64_t end = (seg + 1) * kSeg;  // inside the list: the run goes on there
-    const uint32_t k = p.key[end];
-    // the run's last segment: 32 probes of the sorted list at a time
-    int64_t lo = end, hi = p.tokens;  // key[lo] == k; past hi it is not
-    while (hi - lo > 1) {
-      const int64_t step = (hi - lo + 32) / 33;
-      const int64_t at = lo + step * (lane + 1);
-      const uint32_t in = __ballot_sync(0xffffffffu, at < hi && p.key[at < hi ? at : lo] == k);
-      const int c = __popc(in);
-      hi = min(hi, lo + step * (c + 1));
-      lo += step * c;
+    const uint32_t k = p.key[(seg + 1) * kSeg];  // inside the list: the run goes on there
+    // the run's last segment: the next 32 segments' first keys, then 32 probes at a time
+    const int64_t segs = (p.tokens + kSeg - 1) / kSeg;
+    auto of_run = [&](int64_t s) { return s < segs && p.key[s * kSeg] == k; };
+    int64_t last = seg + 1 + __popc(__ballot_sync(0xffffffffu, of_run(seg + 2 + lane)));
+    if (last == seg + 33) {
+      int64_t hi = segs;  // past hi it is not the run
+      while (hi - last > 1) {
+        const int64_t step = (hi - last + 32) / 33;
+        const int64_t at = last + step * (lane + 1);
+        const int n = __popc(__ballot_sync(0xffffffffu, at < hi && of_run(at)));
+        hi = min(hi, last + step * (n + 1));
+        last += step * n;
+      }
     }
-    const int64_t last = lo / kSeg;
-    const int64_t c = (item % blocks) * kJoinCols + l;
-    float a = 0.f;
-    if (c < p.features) {
-      if (g == 0) a = p.parts[(2 * seg + 1) * p.features + c];
-#pragma unroll 4
-      for (int64_t s = seg + 1 + g; s <= last; s += kJoinGroups) a += p.parts[2 * s * p.features + c];
-    }
-    sh[g][l] = a;
-    __syncthreads();
-    if (g == 0 && c < p.features) {
-      a = 0.f;
+    const int64_t c = ((item % blocks) * kJoinCols + l) * V;
+    float a[V];
 #pragma unroll
-      for (int i = 0; i < kJoinGroups; ++i) a += sh[i][l];
-      float* to = p.dtable + (int64_t)k * p.ldt + c;
-      *to = a * p.scale + (p.accumulate ? *to : 0.f);
+    for (int i = 0; i < V; ++i) a[i] = 0.f;
+    auto add = [&](const float* from) {
+      if (V4) {
+        const float4 v = *reinterpret_cast<const float4*>(from);
+        a[0] += v.x; a[V4 ? 1 : 0] += v.y; a[V4 ? 2 : 0] += v.z; a[V4 ? 3 : 0] += v.w;
+      } else {
+        a[0] += *from;
+      }
+    };
+    if (c < p.features) {
+      if (g == 0) add(p.parts + (2 * seg + 1) * p.features + c);
+#pragma unroll 8
+      for (int64_t s = seg + 1 + g; s <= last; s += kJoinGroups) add(p.parts + 2 * s * p.features + c);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) sh[g][l * V + i] = a[i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < kJoinCols * V; i += kJoinCols * kJoinGroups) {
+      const int64_t col = (item % blocks) * (kJoinCols * V) + i;
+      if (col >= p.features) continue;
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < kJoinGroups; ++j) sum += sh[j][i];
+      float* to = p.dtable + (int64_t)k * p.ldt + col;
+      *to = sum * p.scale + (p.accumulate ? *to : 0.f);
     }
     __syncthreads();
   }
@@ -649,15 +712,16 @@ dion_status embed_grad_impl(const dion_embed_grad* a, void* ws, size_t ws_bytes,
   while (bits < 32 && (a->vocab >> bits) != 0) ++bits;
   const int passes = (bits + kDigit - 1) / kDigit;
   int at = 0;
-  if (a->tokens <= kSmall && a->vocab < kSmallVocab) {
-    constexpr int bytes = (kSmall + kSmallWarps * kBins) * 4;
-    const cudaError_t e = cudaFuncSetAttribute(k_sort_small, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return set_error(DION_ERR_CUDA, "k_sort_small: %s", cudaGetErrorString(e));
+  int pos_bits = 1;
+  while ((a->tokens - 1) >> pos_bits) ++pos_bits;
+  if (a->tokens <= kClusterMost && bits + pos_bits <= 32) {
     sp.first = 1;
     sp.key_out = key[0];
     sp.val_out = val[0];
-    k_sort_small<<<1, kSmallThreads, bytes, s>>>(sp, passes);
-    DION_TRY(launch_status("k_sort_small"));
+    const int per_round = kClusterCtas * kClusterThreads;
+    k_sort_cluster<<<kClusterCtas, kClusterThreads, 0, s>>>(sp, passes, pos_bits,
+                                                            (int)((a->tokens + per_round - 1) / per_round));
+    DION_TRY(launch_status("k_sort_cluster"));
   } else {
     for (int pass = 0; pass < passes; ++pass, at ^= 1) {
       sp.first = pass == 0;
@@ -696,7 +760,9 @@ dion_status embed_grad_impl(const dion_embed_grad* a, void* ws, size_t ws_bytes,
   }
   DION_TRY(launch_status("k_embed_sum"));
   if (g.segs > 1) {
-    k_embed_join<<<(unsigned)(sms * 4), kJoinCols * kJoinGroups, 0, s>>>(p);
+    // the list is on the device: a grid that fills the SMs, whose CTAs leave at once without work
+    if (p.vec_table) k_embed_join<true><<<(unsigned)(sms * 4), kJoinCols * kJoinGroups, 0, s>>>(p);
+    else k_embed_join<false><<<(unsigned)(sms * 4), kJoinCols * kJoinGroups, 0, s>>>(p);
     DION_TRY(launch_status("k_embed_join"));
   }
   return DION_OK;

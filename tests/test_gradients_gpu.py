@@ -432,7 +432,8 @@ def _ids(kind, t, v, seed):
 @pytest.mark.parametrize("t,v,d,pad", [(1, 1, 8, 0), (31, 5, 24, 0), (33, 300, 40, 8), (64, 2, 7, 0),
                                        (1000, 70000, 16, 0), (5000, 257, 130, 2), (9001, 40, 2064, 0),
                                        (16384, 255, 520, 0), (16385, 3000, 24, 0), (500, 300000, 8, 0),
-                                       (130, 262143, 8, 0), (70, 1030, 1032, 0)])
+                                       (130, 262143, 8, 0), (70, 1030, 1032, 0), (32768, 131071, 8, 0),
+                                       (32769, 90, 16, 0), (4097, 65535, 8, 0)])
 def test_embed_grad(t, v, d, pad, kind, dtype):
     ids = _ids(kind, t, v, 3)
     dout = Rows(t, d, DT[dtype], pad, 0, fill=True, seed=4)
