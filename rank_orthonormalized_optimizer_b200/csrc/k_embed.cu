@@ -256,6 +256,7 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterT
   __shared__ uint32_t sums[kBins / 32];
   const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
   const uint32_t cta = blockIdx.x;    // one cluster: the rank
+  grid_trigger();
   const uint32_t share = (uint32_t)rounds * kClusterThreads;
   const int first = w * 32 * rounds + l;
   if (cta == 0 && threadIdx.x == 0) *p.nspans = 0;
@@ -434,6 +435,7 @@ __device__ __forceinline__ void write_zeros(const GradP& p, int64_t first) {
 
 template <typename T, int NT, bool AL>
 __global__ void __launch_bounds__(NT) k_embed_sum(const GradP p) {
+  grid_wait();
   if (blockIdx.x >= p.sum_ctas) {
     write_zeros<NT>(p, (blockIdx.x - p.sum_ctas) * p.zero_rows);
     return;
@@ -450,7 +452,7 @@ __global__ void __launch_bounds__(NT) k_embed_sum(const GradP p) {
     if (i >= 1 && i <= n) val[i - 1] = p.val[at];
   }
   __syncthreads();
-  constexpr int U = 8;
+  constexpr int U = AL ? 8 : 4;  // rows in flight
   float acc[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) acc[e] = 0.f;
@@ -460,6 +462,17 @@ __global__ void __launch_bounds__(NT) k_embed_sum(const GradP p) {
   for (int i0 = 0; i0 < n; i0 += U) {
     if (key[i0 + 1] >= p.vocab) break;  // padding, sorted last
     Raw8<T> raw[AL ? U : 1];
+    float one[AL ? 1 : U][8];
+    if (!AL) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int64_t c = grad_col<NT, AL>(col0, e);
+          one[AL ? 0 : u][e] = i0 + u < n && key[i0 + u + 1] < p.vocab && c < p.features
+                                   ? to_float(dout[val[i0 + u] * p.ldo + c]) : 0.f;
+        }
+    }
     if (AL) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -476,8 +489,7 @@ __global__ void __launch_bounds__(NT) k_embed_sum(const GradP p) {
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int64_t c = grad_col<NT, AL>(col0, e);
-          v[e] = c < p.features ? to_float(dout[val[i] * p.ldo + c]) : 0.f;
+          v[e] = one[AL ? 0 : u][e];
         }
       }
 #pragma unroll
@@ -509,6 +521,7 @@ __global__ void __launch_bounds__(kJoinCols * kJoinGroups) k_embed_join(const Gr
   constexpr int V = V4 ? 4 : 1;
   __shared__ float sh[kJoinGroups][kJoinCols * V];
   const int64_t blocks = (p.features + kJoinCols * V - 1) / (kJoinCols * V);
+  grid_wait();
   const int64_t items = *p.nspans * blocks;
   const int g = threadIdx.x / kJoinCols, l = threadIdx.x % kJoinCols, lane = threadIdx.x & 31;
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
@@ -660,19 +673,20 @@ dion_status lookup_impl(const dion_embed* a, void* stream) {
 
 // Threads of a segment's CTA: a warp's worth of 8 columns each up to 256 columns, at most 256.
 template <typename T>
-void launch_sum(GradP p, bool al, int64_t segs, cudaStream_t s) {
+cudaError_t launch_sum(GradP p, bool al, int64_t segs, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
   auto go = [&](auto nt) {
     constexpr int NT = decltype(nt)::value;
     p.col_ctas = (int)((p.features + 8 * NT - 1) / (8 * NT));
     p.sum_ctas = segs * p.col_ctas;
     const int64_t grid = p.sum_ctas + (p.accumulate ? 0 : (p.vocab + p.zero_rows - 1) / p.zero_rows);
-    if (al) k_embed_sum<T, NT, true><<<(unsigned)grid, NT, 0, s>>>(p);
-    else k_embed_sum<T, NT, false><<<(unsigned)grid, NT, 0, s>>>(p);
+    e = launch_after(al ? k_embed_sum<T, NT, true> : k_embed_sum<T, NT, false>, dim3((unsigned)grid), NT, 0, s, p);
   };
   if (p.features <= 256) go(std::integral_constant<int, 32>());
   else if (p.features <= 512) go(std::integral_constant<int, 64>());
   else if (p.features <= 1024) go(std::integral_constant<int, 128>());
   else go(std::integral_constant<int, 256>());
+  return e;
 }
 
 dion_status embed_grad_impl(const dion_embed_grad* a, void* ws, size_t ws_bytes, void* stream) {
@@ -753,17 +767,13 @@ dion_status embed_grad_impl(const dion_embed_grad* a, void* ws, size_t ws_bytes,
   // 128 KB of zeros to a CTA: enough to pay for finding its rows in the list
   p.zero_rows = (int)std::max<int64_t>(1, std::min<int64_t>(kZeroRows, (128 << 10) / (4 * a->features)));
   const bool al = a->features % 8 == 0 && p.vec_table && rows_aligned16(a->dout, a->ldo, es);
-  switch (a->dtype) {
-    case DION_BF16: launch_sum<__nv_bfloat16>(p, al, g.segs, s); break;
-    case DION_FP16: launch_sum<__half>(p, al, g.segs, s); break;
-    default: launch_sum<float>(p, al, g.segs, s);
-  }
-  DION_TRY(launch_status("k_embed_sum"));
+  DION_TRY(launch_status("k_embed_sum", a->dtype == DION_BF16   ? launch_sum<__nv_bfloat16>(p, al, g.segs, s)
+                                        : a->dtype == DION_FP16 ? launch_sum<__half>(p, al, g.segs, s)
+                                                                : launch_sum<float>(p, al, g.segs, s)));
   if (g.segs > 1) {
     // the list is on the device: a grid that fills the SMs, whose CTAs leave at once without work
-    if (p.vec_table) k_embed_join<true><<<(unsigned)(sms * 4), kJoinCols * kJoinGroups, 0, s>>>(p);
-    else k_embed_join<false><<<(unsigned)(sms * 4), kJoinCols * kJoinGroups, 0, s>>>(p);
-    DION_TRY(launch_status("k_embed_join"));
+    DION_TRY(launch_status("k_embed_join", launch_after(p.vec_table ? k_embed_join<true> : k_embed_join<false>,
+                                                        dim3((unsigned)(sms * 4)), kJoinCols * kJoinGroups, 0, s, p)));
   }
   return DION_OK;
 }

@@ -425,6 +425,7 @@ __global__ void __launch_bounds__(cta_threads(NT), ctas_per_sm(NT)) k_norm_grad_
   constexpr int E = 8 * VPT, RPC = NT == 32 ? kWarpRows : 1;
   extern __shared__ uint4 ring_smem[];
   __shared__ float red[NT == 32 ? 1 : 3 * NT / 32];
+  grid_trigger();  // a grid of one round, whose CTAs fill the SMs
   enum { H, DU, DH, Y };
   const Ring<T, NT, VPT, 4> ring(ring_smem);
   const int tid = NT == 32 ? threadIdx.x & 31 : threadIdx.x;
@@ -678,6 +679,7 @@ __global__ void __launch_bounds__(kGainThreads) k_norm_gains(const GainP p) {
   const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
   const int c = blockIdx.x * COLS + l % COLS;
   float a = 0.f, b = 0.f;
+  grid_wait();
   if (c < p.features) {
 #pragma unroll 4
     for (int k = threadIdx.x / COLS; k < p.nparts; k += kGainThreads / COLS) {
@@ -935,9 +937,10 @@ dion_status norm_grad_impl(const dion_norm_grad* a, void* ws, size_t ws_bytes, v
   // no rows: the sums are zero (added to nothing, or written as zeros)
   const GainP gp{static_cast<const float*>(ws), (int)grid, (int)a->features, a->post_gain, a->gate,
                  a->dpre_gain, a->dpost_gain, a->dgate, a->residual_scale, a->accumulate != 0};
-  if (a->features >= 4096) k_norm_gains<32><<<(unsigned)((a->features + 31) / 32), kGainThreads, 0, s>>>(gp);
-  else k_norm_gains<8><<<(unsigned)((a->features + 7) / 8), kGainThreads, 0, s>>>(gp);
-  return launch_status("k_norm_gains");
+  const int cols = a->features >= 4096 ? 32 : 8;
+  return launch_status("k_norm_gains",
+                       launch_after(cols == 32 ? k_norm_gains<32> : k_norm_gains<8>,
+                                    dim3((unsigned)((a->features + cols - 1) / cols)), kGainThreads, 0, s, gp));
 }
 
 }  // namespace

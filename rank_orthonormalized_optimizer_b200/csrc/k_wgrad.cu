@@ -256,6 +256,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  grid_trigger();  // a grid of one round: the join's CTAs come as these end
   if (warp < 4) {
     reg_dec<40>();
     if ((warp == 0 || warp == 2) && lane == 0) {
@@ -533,6 +534,7 @@ __global__ void __launch_bounds__(256) k_wgrad_join(const WgradP p, int bn) {
   const int i0 = blockIdx.y * 32, j0 = blockIdx.x * 32;
   const int64_t row0 = (int64_t)(tile % p.tiles_m) * PM + i0, col0 = (int64_t)(tile / p.tiles_m) * bn + j0;
   if (row0 >= p.m || col0 >= p.n) return;
+  grid_wait();
   const int64_t plane = (int64_t)PM * bn;
   const float* from = p.parts + blockIdx.z * p.splits * plane + (int64_t)i0 * bn + j0;
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -742,8 +744,8 @@ dion_status one_grad(const dion_grad_source& src, int accumulate, char* ws, int3
   p.max_spins = kMaxSpins;
   const dion_status st = g.bn == 256 ? launch<256>(mq, md, p, sms, s) : launch<128>(mq, md, p, sms, s);
   if (st != DION_OK || g.tail == 0) return st;
-  k_wgrad_join<<<dim3((unsigned)(g.bn / 32), PM / 32, (unsigned)g.tail), 256, 0, s>>>(p, g.bn);
-  return launch_status("k_wgrad_join");
+  return launch_status("k_wgrad_join", launch_after(k_wgrad_join, dim3((unsigned)(g.bn / 32), PM / 32, (unsigned)g.tail),
+                                                    256, 0, s, p, g.bn));
 }
 
 dion_status wgrad_impl(const dion_grad_source* src, int32_t nsrc, int32_t accumulate, void* ws,

@@ -35,10 +35,28 @@ inline dion_status check_sm100(int* sms) {
   return DION_OK;
 }
 
-inline dion_status launch_status(const char* what) {
-  const cudaError_t e = cudaGetLastError();
+inline dion_status launch_status(const char* what, cudaError_t e = cudaGetLastError()) {
   return e == cudaSuccess ? DION_OK
                           : set_error(DION_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+// Launch a kernel that starts with grid_wait(): its CTAs are set up while the kernel before it
+// on the stream still runs.  (After a kernel that calls grid_trigger() they may also wait on
+// idle SMs; without it they come as that kernel's CTAs end.)
+template <typename... P, typename... A>
+inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem,
+                                cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = attr;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, P(args)...);
 }
 
 inline bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
