@@ -9,6 +9,8 @@
 #include "operator.h"
 #include "rows.cuh"
 
+#include <algorithm>
+
 namespace dion {
 namespace {
 
@@ -23,27 +25,27 @@ struct ActP {
   int64_t tokens, features, ld;  // ld = features rounded up to 32
 };
 
-template <typename T>
+template <typename T, typename I>
 __global__ void __launch_bounds__(kThreads) k_act_save(const ActP p) {
-  const int64_t per_row = p.ld / 8, total = p.tokens * per_row;
+  const I per_row = (I)(p.ld / 8), total = (I)(p.tokens * per_row);
   const T* x = static_cast<const T*>(p.x);
-  const int64_t stride = (int64_t)gridDim.x * kThreads;
+  const I stride = (I)gridDim.x * kThreads;
   // whole groups of four lanes share a block: the loop runs to a multiple of 32
-  const int64_t end = (total + 31) / 32 * 32;
-  for (int64_t i0 = (int64_t)blockIdx.x * kThreads + threadIdx.x; i0 < end; i0 += stride * kUnroll) {
+  const I end = (total + 31) / 32 * 32;
+  for (I i0 = (I)blockIdx.x * kThreads + threadIdx.x; i0 < end; i0 += stride * kUnroll) {
     Raw8<T> raw[kUnroll];
     int64_t row[kUnroll];
     int col[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int64_t i = i0 + u * stride;
-      row[u] = i / per_row;
-      col[u] = (int)(i - row[u] * per_row) * 8;
+      const I i = i0 + u * stride, r = i / per_row;
+      row[u] = r;
+      col[u] = (int)(i - r * per_row) * 8;
       raw[u] = (i < total && col[u] < p.features) ? load_raw(x + row[u] * p.ldx + col[u]) : zero_raw<T>();
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int64_t i = i0 + u * stride;
+      const I i = i0 + u * stride;
       float v[8];
       unpack(raw[u], v);
       uint32_t top = 0;
@@ -67,14 +69,14 @@ __global__ void __launch_bounds__(kThreads) k_act_save(const ActP p) {
   }
 }
 
-template <typename T>
+template <typename T, typename I>
 __global__ void __launch_bounds__(kThreads) k_act_save_any(const ActP p) {
-  const int64_t per_row = p.ld / 32, total = p.tokens * per_row;
+  const I per_row = (I)(p.ld / 32), total = (I)(p.tokens * per_row);
   const T* x = static_cast<const T*>(p.x);
   const int lane = threadIdx.x & 31;
-  for (int64_t b = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / 32; b < total;
-       b += (int64_t)gridDim.x * kThreads / 32) {
-    const int64_t row = b / per_row, col = (b - row * per_row) * 32 + lane;
+  for (I b = ((I)blockIdx.x * kThreads + threadIdx.x) / 32; b < total; b += (I)gridDim.x * kThreads / 32) {
+    const I r = b / per_row;
+    const int64_t row = r, col = (int64_t)(b - r * per_row) * 32 + lane;
     const float v = col < p.features ? to_float(x[row * p.ldx + col]) : 0.f;
     const uint32_t top = __reduce_max_sync(0xffffffffu, abs_bits(v));
     const int e = act_exponent(top);
@@ -84,21 +86,21 @@ __global__ void __launch_bounds__(kThreads) k_act_save_any(const ActP p) {
   }
 }
 
-template <typename T>
+template <typename T, typename I>
 __global__ void __launch_bounds__(kThreads) k_act_load(const ActP p) {
-  const int64_t per_row = p.ld / 8, total = p.tokens * per_row;
+  const I per_row = (I)(p.ld / 8), total = (I)(p.tokens * per_row);
   T* x = static_cast<T*>(const_cast<void*>(p.x));
-  const int64_t stride = (int64_t)gridDim.x * kThreads;
-  for (int64_t i0 = (int64_t)blockIdx.x * kThreads + threadIdx.x; i0 < total; i0 += stride * kUnroll) {
+  const I stride = (I)gridDim.x * kThreads;
+  for (I i0 = (I)blockIdx.x * kThreads + threadIdx.x; i0 < total; i0 += stride * kUnroll) {
     uint2 raw[kUnroll];
     uint32_t E[kUnroll];
     int64_t row[kUnroll];
     int col[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int64_t i = i0 + u * stride;
-      row[u] = i / per_row;
-      col[u] = (int)(i - row[u] * per_row) * 8;
+      const I i = i0 + u * stride, r = i / per_row;
+      row[u] = r;
+      col[u] = (int)(i - r * per_row) * 8;
       if (i < total && col[u] < p.features) {
         raw[u] = *reinterpret_cast<const uint2*>(p.q + row[u] * p.ld + col[u]);
         E[u] = p.scale[row[u] * (p.ld / 32) + col[u] / 32];
@@ -106,7 +108,7 @@ __global__ void __launch_bounds__(kThreads) k_act_load(const ActP p) {
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int64_t i = i0 + u * stride;
+      const I i = i0 + u * stride;
       if (i >= total || col[u] >= p.features) continue;
       const float f = act_scale(E[u]);
       float v[8];
@@ -121,17 +123,28 @@ __global__ void __launch_bounds__(kThreads) k_act_load(const ActP p) {
   }
 }
 
-template <typename T>
+template <typename T, typename I>
 __global__ void __launch_bounds__(kThreads) k_act_load_any(const ActP p) {
-  const int64_t per_row = p.ld / 32, total = p.tokens * per_row;
+  const I per_row = (I)(p.ld / 32), total = (I)(p.tokens * per_row);
   T* x = static_cast<T*>(const_cast<void*>(p.x));
   const int lane = threadIdx.x & 31;
-  for (int64_t b = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / 32; b < total;
-       b += (int64_t)gridDim.x * kThreads / 32) {
-    const int64_t row = b / per_row, col = (b - row * per_row) * 32 + lane;
+  for (I b = ((I)blockIdx.x * kThreads + threadIdx.x) / 32; b < total; b += (I)gridDim.x * kThreads / 32) {
+    const I r = b / per_row;
+    const int64_t row = r, col = (int64_t)(b - r * per_row) * 32 + lane;
     if (col < p.features)
       x[row * p.ldx + col] =
           from_float<T>(e4m3x2_float(p.q[row * p.ld + col]).x * act_scale(p.scale[b]));
+  }
+}
+
+template <typename T, typename I>
+void launch_as(const ActP& p, bool save, bool vec, unsigned grid, cudaStream_t s) {
+  if (save) {
+    if (vec) k_act_save<T, I><<<grid, kThreads, 0, s>>>(p);
+    else k_act_save_any<T, I><<<grid, kThreads, 0, s>>>(p);
+  } else {
+    if (vec) k_act_load<T, I><<<grid, kThreads, 0, s>>>(p);
+    else k_act_load_any<T, I><<<grid, kThreads, 0, s>>>(p);
   }
 }
 
@@ -139,18 +152,14 @@ template <typename T>
 dion_status launch(const ActP& p, bool save, int sms, cudaStream_t s) {
   // the vector form takes whole 8-element groups of 16-byte aligned rows
   const bool vec = rows_aligned16(p.x, p.ldx, sizeof(T)) && p.features % 8 == 0;
-  const int64_t work = vec ? p.tokens * (p.ld / 8) : p.tokens * p.ld;  // threads' worth
-  const int64_t cap = (int64_t)sms * 8;
+  const int64_t items = vec ? p.tokens * (p.ld / 8) : p.tokens * p.ld;  // a thread's each
+  const int64_t cap = (int64_t)sms * (vec ? 8 : 32);
   const int64_t per_cta = vec ? kThreads * kUnroll : kThreads;
-  const int64_t want = (work + per_cta - 1) / per_cta;
-  const unsigned grid = (unsigned)(vec || want < cap * 4 ? (want < cap ? want : cap) : cap * 4);
-  if (save) {
-    if (vec) k_act_save<T><<<grid, kThreads, 0, s>>>(p);
-    else k_act_save_any<T><<<grid, kThreads, 0, s>>>(p);
-  } else {
-    if (vec) k_act_load<T><<<grid, kThreads, 0, s>>>(p);
-    else k_act_load_any<T><<<grid, kThreads, 0, s>>>(p);
-  }
+  const unsigned grid = (unsigned)std::min((items + per_cta - 1) / per_cta, cap);
+  // indexes in 32 bits where all of them fit (a loop's last step overshoots by its stride):
+  // the division by the row length is what costs
+  if (items + cap * kThreads * kUnroll < (int64_t(1) << 31)) launch_as<T, uint32_t>(p, save, vec, grid, s);
+  else launch_as<T, int64_t>(p, save, vec, grid, s);
   return launch_status(save ? "k_act_save" : "k_act_load");
 }
 

@@ -47,21 +47,22 @@ __device__ __forceinline__ int64_t load_id(const void* ids, int id64, int64_t t)
 }
 
 // One item: VEC consecutive elements of an output row.
-template <typename TI, typename TO, int VEC>
+constexpr int kLookups = 4;  // items of a thread in flight
+template <typename TI, typename TO, int VEC, typename I>
 __global__ void __launch_bounds__(kThreads) k_embed_lookup(const LookupP p) {
-  constexpr int U = 4;
-  const int64_t per_row = p.features / VEC, total = p.tokens * per_row;
-  const int64_t stride = (int64_t)gridDim.x * kThreads;
+  constexpr int U = kLookups;
+  const I per_row = (I)(p.features / VEC), total = (I)(p.tokens * per_row);
+  const I stride = (I)gridDim.x * kThreads;
   const TI* table = static_cast<const TI*>(p.table);
   TO* out = static_cast<TO*>(p.out);
-  for (int64_t i0 = (int64_t)blockIdx.x * kThreads + threadIdx.x; i0 < total; i0 += stride * U) {
+  for (I i0 = (I)blockIdx.x * kThreads + threadIdx.x; i0 < total; i0 += stride * U) {
     int64_t row[U], id[U];
     int64_t col[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t i = i0 + u * stride;
-      row[u] = i / per_row;
-      col[u] = (i - row[u] * per_row) * VEC;
+      const I i = i0 + u * stride, r = i / per_row;
+      row[u] = r;
+      col[u] = (int64_t)(i - r * per_row) * VEC;
       id[u] = i < total ? load_id(p.ids, p.id64, row[u]) : -1;
     }
     if (VEC == 8) {
@@ -96,8 +97,11 @@ void launch_lookup(const LookupP& p, bool vec, int sms, cudaStream_t s) {
   const int64_t items = p.tokens * (vec ? p.features / 8 : p.features);
   const int64_t want = (items + kThreads - 1) / kThreads, cap = (int64_t)sms * 8;
   const unsigned grid = (unsigned)(want < cap ? want : cap);
-  if (vec) k_embed_lookup<TI, TO, 8><<<grid, kThreads, 0, s>>>(p);
-  else k_embed_lookup<TI, TO, 1><<<grid, kThreads, 0, s>>>(p);
+  // as the 8-bit form's: 32-bit indexes where they fit
+  const bool small = items + cap * kThreads * kLookups < (int64_t(1) << 31);
+  auto* kernel = vec ? (small ? k_embed_lookup<TI, TO, 8, uint32_t> : k_embed_lookup<TI, TO, 8, int64_t>)
+                     : (small ? k_embed_lookup<TI, TO, 1, uint32_t> : k_embed_lookup<TI, TO, 1, int64_t>);
+  kernel<<<grid, kThreads, 0, s>>>(p);
 }
 
 // ---------------------------------------------------------------- sort
