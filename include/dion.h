@@ -450,8 +450,8 @@ int32_t dion_vec_last_launch_count(void);
  *  - tokens may be 0.  Gains and gradients of gains are contiguous fp32 arrays.
  *  - arguments are checked before anything is enqueued; the work is enqueued on `stream`
  *    of the current device, and the call returns.  No entry point allocates device memory
- *    or synchronises.  A workspace needs no clearing and no keeping between calls, and must
- *    not be shared by two calls in flight.
+ *    or synchronises.  A workspace is aligned to 32 bytes, needs no clearing and no keeping
+ *    between calls, and must not be shared by two calls in flight.
  *  - `accumulate` != 0 adds to the gradient that is there (a further micro-batch);
  *    0 overwrites it.
  *  - results repeat bit for bit: no sum is taken by floating-point atomics.

@@ -3,9 +3,9 @@
 // A block of 32 features of a token becomes 32 e4m3 bytes and one exponent byte (the rule
 // stands in rows.cuh): 33 bytes where bf16 takes 64.  Both directions are one pass over
 // HBM with no reuse, 3.03 bytes per bf16 element; what bounds them is the copy bandwidth.
-// Rows that start on 16 bytes move 8 elements a thread (four neighbouring lanes share a
-// block, so its maximum takes two shuffles), kUnroll of them in flight; other rows go one
-// element a lane, a warp to a block.
+// A thread moves 32 bytes of a row (16 elements of the 2-byte types, so two neighbouring lanes
+// share a block and its maximum takes a shuffle), 16 where the rows only start on 16 bytes,
+// kUnroll pieces in flight; other rows go one element a lane, a warp to a block.
 #include "operator.h"
 #include "rows.cuh"
 
@@ -25,57 +25,70 @@ struct ActP {
   int64_t tokens, features, ld;  // ld = features rounded up to 32
 };
 
-template <typename T, typename I>
-__global__ void __launch_bounds__(kThreads) k_act_save(const ActP p) {
-  const I per_row = (I)(p.ld / 8), total = (I)(p.tokens * per_row);
+// 8 H elements at 16 H bytes (2-byte types) or, H = 1, 32 bytes (fp32).
+template <typename T, int H>
+__device__ __forceinline__ void load_pieces(const T* p, Raw8<T>* raw) {
+  if constexpr (H == 2) ld_stream32(p, raw[0].a, raw[1].a);
+  else raw[0] = load_raw(p);
+}
+
+template <typename T, typename I, int H>
+__global__ void __launch_bounds__(kThreads) k_act_save(const ActP p, const RowDiv<I> row_of) {
+  constexpr int N = 8 * H;
+  const I per_row = (I)(p.ld / N), total = (I)(p.tokens * per_row);
   const T* x = static_cast<const T*>(p.x);
   const I stride = (I)gridDim.x * kThreads;
-  // whole groups of four lanes share a block: the loop runs to a multiple of 32
+  // whole groups of lanes share a block: the loop runs to a multiple of 32
   const I end = (total + 31) / 32 * 32;
   for (I i0 = (I)blockIdx.x * kThreads + threadIdx.x; i0 < end; i0 += stride * kUnroll) {
-    Raw8<T> raw[kUnroll];
+    Raw8<T> raw[kUnroll][H];
     int64_t row[kUnroll];
     int col[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const I i = i0 + u * stride, r = i / per_row;
+      const I i = i0 + u * stride, r = row_of(i);
       row[u] = r;
-      col[u] = (int)(i - r * per_row) * 8;
-      raw[u] = (i < total && col[u] < p.features) ? load_raw(x + row[u] * p.ldx + col[u]) : zero_raw<T>();
+      col[u] = (int)(i - r * per_row) * N;
+      if (i < total && col[u] < p.features) load_pieces<T, H>(x + row[u] * p.ldx + col[u], raw[u]);
+      else
+#pragma unroll
+        for (int h = 0; h < H; ++h) raw[u][h] = zero_raw<T>();
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const I i = i0 + u * stride;
-      float v[8];
-      unpack(raw[u], v);
-      uint32_t top = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) top = max(top, abs_bits(v[j]));
+      uint32_t top = abs_bits8(raw[u][0]);
+      if (H == 2) top = max(top, abs_bits8(raw[u][H - 1]));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      if (H == 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int e = act_exponent(top);
       const float f = act_unscale(e);
       const bool fine = top < kInfBits;
+      uint32_t o[2 * H];
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        float v[8];
+        unpack(raw[u][h], v);
+        o[2 * h] = fine ? e4m3x2(v[0] * f, v[1] * f) | e4m3x2(v[2] * f, v[3] * f) << 16 : 0u;
+        o[2 * h + 1] = fine ? e4m3x2(v[4] * f, v[5] * f) | e4m3x2(v[6] * f, v[7] * f) << 16 : 0u;
+      }
       if (i < total) {
-        uint2 o = make_uint2(0, 0);
-        if (fine) {
-          o.x = e4m3x2(v[0] * f, v[1] * f) | e4m3x2(v[2] * f, v[3] * f) << 16;
-          o.y = e4m3x2(v[4] * f, v[5] * f) | e4m3x2(v[6] * f, v[7] * f) << 16;
-        }
-        *reinterpret_cast<uint2*>(p.q + row[u] * p.ld + col[u]) = o;
-        if ((i & 3) == 0) p.scale[row[u] * (p.ld / 32) + col[u] / 32] = fine ? e + 127 : 255;
+        uint8_t* q = p.q + row[u] * p.ld + col[u];
+        if constexpr (H == 2) st_vec(q, make_uint4(o[0], o[1], o[2], o[3]));
+        else *reinterpret_cast<uint2*>(q) = make_uint2(o[0], o[1]);
+        if (i % (4 / H) == 0) p.scale[row[u] * (p.ld / 32) + col[u] / 32] = fine ? e + 127 : 255;
       }
     }
   }
 }
 
 template <typename T, typename I>
-__global__ void __launch_bounds__(kThreads) k_act_save_any(const ActP p) {
+__global__ void __launch_bounds__(kThreads) k_act_save_any(const ActP p, const RowDiv<I> row_of) {
   const I per_row = (I)(p.ld / 32), total = (I)(p.tokens * per_row);
   const T* x = static_cast<const T*>(p.x);
   const int lane = threadIdx.x & 31;
   for (I b = ((I)blockIdx.x * kThreads + threadIdx.x) / 32; b < total; b += (I)gridDim.x * kThreads / 32) {
-    const I r = b / per_row;
+    const I r = row_of(b);
     const int64_t row = r, col = (int64_t)(b - r * per_row) * 32 + lane;
     const float v = col < p.features ? to_float(x[row * p.ldx + col]) : 0.f;
     const uint32_t top = __reduce_max_sync(0xffffffffu, abs_bits(v));
@@ -86,23 +99,31 @@ __global__ void __launch_bounds__(kThreads) k_act_save_any(const ActP p) {
   }
 }
 
-template <typename T, typename I>
-__global__ void __launch_bounds__(kThreads) k_act_load(const ActP p) {
-  const I per_row = (I)(p.ld / 8), total = (I)(p.tokens * per_row);
+template <typename T, typename I, int H>
+__global__ void __launch_bounds__(kThreads) k_act_load(const ActP p, const RowDiv<I> row_of) {
+  constexpr int N = 8 * H;
+  const I per_row = (I)(p.ld / N), total = (I)(p.tokens * per_row);
   T* x = static_cast<T*>(const_cast<void*>(p.x));
   const I stride = (I)gridDim.x * kThreads;
   for (I i0 = (I)blockIdx.x * kThreads + threadIdx.x; i0 < total; i0 += stride * kUnroll) {
-    uint2 raw[kUnroll];
+    uint32_t raw[kUnroll][2 * H];
     uint32_t E[kUnroll];
     int64_t row[kUnroll];
     int col[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const I i = i0 + u * stride, r = i / per_row;
+      const I i = i0 + u * stride, r = row_of(i);
       row[u] = r;
-      col[u] = (int)(i - r * per_row) * 8;
+      col[u] = (int)(i - r * per_row) * N;
       if (i < total && col[u] < p.features) {
-        raw[u] = *reinterpret_cast<const uint2*>(p.q + row[u] * p.ld + col[u]);
+        const uint8_t* q = p.q + row[u] * p.ld + col[u];
+        if constexpr (H == 2) {
+          const uint4 v = ld_stream(q);
+          raw[u][0] = v.x; raw[u][1] = v.y; raw[u][2 * H - 2] = v.z; raw[u][2 * H - 1] = v.w;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(q);
+          raw[u][0] = v.x; raw[u][1] = v.y;
+        }
         E[u] = p.scale[row[u] * (p.ld / 32) + col[u] / 32];
       }
     }
@@ -111,25 +132,27 @@ __global__ void __launch_bounds__(kThreads) k_act_load(const ActP p) {
       const I i = i0 + u * stride;
       if (i >= total || col[u] >= p.features) continue;
       const float f = act_scale(E[u]);
-      float v[8];
+      float v[N];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 t = e4m3x2_float(((j < 2 ? raw[u].x : raw[u].y) >> (16 * (j & 1))) & 0xffffu);
+      for (int j = 0; j < N / 2; ++j) {
+        const float2 t = e4m3x2_float((raw[u][j / 2] >> (16 * (j & 1))) & 0xffffu);
         v[2 * j] = t.x * f;
         v[2 * j + 1] = t.y * f;
       }
-      store8(x + row[u] * p.ldx + col[u], v);
+      T* to = x + row[u] * p.ldx + col[u];
+      if constexpr (H == 2) st_vec32(to, pack8(v, T()), pack8(v + 8, T()));
+      else store8(to, v);
     }
   }
 }
 
 template <typename T, typename I>
-__global__ void __launch_bounds__(kThreads) k_act_load_any(const ActP p) {
+__global__ void __launch_bounds__(kThreads) k_act_load_any(const ActP p, const RowDiv<I> row_of) {
   const I per_row = (I)(p.ld / 32), total = (I)(p.tokens * per_row);
   T* x = static_cast<T*>(const_cast<void*>(p.x));
   const int lane = threadIdx.x & 31;
   for (I b = ((I)blockIdx.x * kThreads + threadIdx.x) / 32; b < total; b += (I)gridDim.x * kThreads / 32) {
-    const I r = b / per_row;
+    const I r = row_of(b);
     const int64_t row = r, col = (int64_t)(b - r * per_row) * 32 + lane;
     if (col < p.features)
       x[row * p.ldx + col] =
@@ -137,29 +160,43 @@ __global__ void __launch_bounds__(kThreads) k_act_load_any(const ActP p) {
   }
 }
 
-template <typename T, typename I>
-void launch_as(const ActP& p, bool save, bool vec, unsigned grid, cudaStream_t s) {
-  if (save) {
-    if (vec) k_act_save<T, I><<<grid, kThreads, 0, s>>>(p);
-    else k_act_save_any<T, I><<<grid, kThreads, 0, s>>>(p);
+template <typename T, typename I, int H>
+void launch_as(const ActP& p, bool save, unsigned grid, cudaStream_t s) {
+  const RowDiv<I> row_of(H > 0 ? p.ld / (8 * H) : p.ld / 32);
+  if constexpr (H > 0) {
+    if (save) k_act_save<T, I, H><<<grid, kThreads, 0, s>>>(p, row_of);
+    else k_act_load<T, I, H><<<grid, kThreads, 0, s>>>(p, row_of);
   } else {
-    if (vec) k_act_load<T, I><<<grid, kThreads, 0, s>>>(p);
-    else k_act_load_any<T, I><<<grid, kThreads, 0, s>>>(p);
+    if (save) k_act_save_any<T, I><<<grid, kThreads, 0, s>>>(p, row_of);
+    else k_act_load_any<T, I><<<grid, kThreads, 0, s>>>(p, row_of);
   }
+}
+
+// H pieces of 8 elements to a thread; 0: the form without vectors.
+template <typename T, int H>
+void launch(const ActP& p, bool save, int sms, cudaStream_t s) {
+  const int64_t items = p.tokens * (H > 0 ? p.ld / (8 * H) : p.ld);  // a thread's each
+  const int64_t cap = (int64_t)sms * (H > 0 ? 8 : 32);
+  const int64_t per_cta = H > 0 ? kThreads * kUnroll : kThreads;
+  const unsigned grid = (unsigned)std::min((items + per_cta - 1) / per_cta, cap);
+  // indexes in 32 bits where all of them fit (a loop's last step overshoots by its stride):
+  // the division by the row length is what costs
+  if (items + cap * kThreads * kUnroll < (int64_t(1) << 31)) launch_as<T, uint32_t, H>(p, save, grid, s);
+  else launch_as<T, int64_t, H>(p, save, grid, s);
 }
 
 template <typename T>
 dion_status launch(const ActP& p, bool save, int sms, cudaStream_t s) {
-  // the vector form takes whole 8-element groups of 16-byte aligned rows
-  const bool vec = rows_aligned16(p.x, p.ldx, sizeof(T)) && p.features % 8 == 0;
-  const int64_t items = vec ? p.tokens * (p.ld / 8) : p.tokens * p.ld;  // a thread's each
-  const int64_t cap = (int64_t)sms * (vec ? 8 : 32);
-  const int64_t per_cta = vec ? kThreads * kUnroll : kThreads;
-  const unsigned grid = (unsigned)std::min((items + per_cta - 1) / per_cta, cap);
-  // indexes in 32 bits where all of them fit (a loop's last step overshoots by its stride):
-  // the division by the row length is what costs
-  if (items + cap * kThreads * kUnroll < (int64_t(1) << 31)) launch_as<T, uint32_t>(p, save, vec, grid, s);
-  else launch_as<T, int64_t>(p, save, vec, grid, s);
+  const bool vec = p.features % 8 == 0 && rows_vector(p.x, p.ldx, sizeof(T));
+  const bool wide = vec && sizeof(T) == 2 && p.features % 16 == 0 && p.ldx % 16 == 0 && aligned_to(p.x, 32);
+  if constexpr (sizeof(T) == 2) {
+    if (wide) launch<T, 2>(p, save, sms, s);
+    else if (vec) launch<T, 1>(p, save, sms, s);
+    else launch<T, 0>(p, save, sms, s);
+  } else {
+    if (vec) launch<T, 1>(p, save, sms, s);
+    else launch<T, 0>(p, save, sms, s);
+  }
   return launch_status(save ? "k_act_save" : "k_act_load");
 }
 

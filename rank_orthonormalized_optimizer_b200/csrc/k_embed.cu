@@ -49,7 +49,7 @@ __device__ __forceinline__ int64_t load_id(const void* ids, int id64, int64_t t)
 // One item: VEC consecutive elements of an output row.
 constexpr int kLookups = 4;  // items of a thread in flight
 template <typename TI, typename TO, int VEC, typename I>
-__global__ void __launch_bounds__(kThreads) k_embed_lookup(const LookupP p) {
+__global__ void __launch_bounds__(kThreads) k_embed_lookup(const LookupP p, const RowDiv<I> row_of) {
   constexpr int U = kLookups;
   const I per_row = (I)(p.features / VEC), total = (I)(p.tokens * per_row);
   const I stride = (I)gridDim.x * kThreads;
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kThreads) k_embed_lookup(const LookupP p) {
     int64_t col[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const I i = i0 + u * stride, r = i / per_row;
+      const I i = i0 + u * stride, r = row_of(i);
       row[u] = r;
       col[u] = (int64_t)(i - r * per_row) * VEC;
       id[u] = i < total ? load_id(p.ids, p.id64, row[u]) : -1;
@@ -99,9 +99,14 @@ void launch_lookup(const LookupP& p, bool vec, int sms, cudaStream_t s) {
   const unsigned grid = (unsigned)(want < cap ? want : cap);
   // as the 8-bit form's: 32-bit indexes where they fit
   const bool small = items + cap * kThreads * kLookups < (int64_t(1) << 31);
-  auto* kernel = vec ? (small ? k_embed_lookup<TI, TO, 8, uint32_t> : k_embed_lookup<TI, TO, 8, int64_t>)
-                     : (small ? k_embed_lookup<TI, TO, 1, uint32_t> : k_embed_lookup<TI, TO, 1, int64_t>);
-  kernel<<<grid, kThreads, 0, s>>>(p);
+  const int64_t per_row = vec ? p.features / 8 : p.features;
+  if (small) {
+    auto* kernel = vec ? k_embed_lookup<TI, TO, 8, uint32_t> : k_embed_lookup<TI, TO, 1, uint32_t>;
+    kernel<<<grid, kThreads, 0, s>>>(p, RowDiv<uint32_t>(per_row));
+  } else {
+    auto* kernel = vec ? k_embed_lookup<TI, TO, 8, int64_t> : k_embed_lookup<TI, TO, 1, int64_t>;
+    kernel<<<grid, kThreads, 0, s>>>(p, RowDiv<int64_t>(per_row));
+  }
 }
 
 // ---------------------------------------------------------------- sort
@@ -656,8 +661,8 @@ dion_status lookup_impl(const dion_embed* a, void* stream) {
   if (a->tokens == 0) return DION_OK;
   const LookupP p{a->table, a->ids, a->out, a->ldt, a->ldo, a->tokens, a->vocab, a->features,
                   a->id_bytes == 8, a->scale};
-  const bool vec = a->features % 8 == 0 && rows_aligned16(a->table, a->ldt, ti) &&
-                   rows_aligned16(a->out, a->ldo, to);
+  const bool vec = a->features % 8 == 0 && rows_vector(a->table, a->ldt, ti) &&
+                   rows_vector(a->out, a->ldo, to);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   auto from = [&](auto in) {
     using TI = decltype(in);
@@ -705,7 +710,7 @@ dion_status embed_grad_impl(const dion_embed_grad* a, void* ws, size_t ws_bytes,
     if (!ws) return set_error(DION_ERR_INVALID_ARG, "workspace is NULL");
     if (ws_bytes < g.bytes)
       return set_error(DION_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes, %zu needed", ws_bytes, g.bytes);
-    if (!aligned_to(ws, 16)) return set_error(DION_ERR_MISALIGNED, "workspace is not 16-byte aligned");
+    if (!aligned_to(ws, 32)) return set_error(DION_ERR_MISALIGNED, "workspace is not 32-byte aligned");
   }
   int sms = 0;
   DION_TRY(check_sm100(&sms));
@@ -770,7 +775,7 @@ dion_status embed_grad_impl(const dion_embed_grad* a, void* ws, size_t ws_bytes,
   p.vec_table = a->features % 4 == 0 && rows_aligned16(a->dtable, a->ldt, 4);
   // 128 KB of zeros to a CTA: enough to pay for finding its rows in the list
   p.zero_rows = (int)std::max<int64_t>(1, std::min<int64_t>(kZeroRows, (128 << 10) / (4 * a->features)));
-  const bool al = a->features % 8 == 0 && p.vec_table && rows_aligned16(a->dout, a->ldo, es);
+  const bool al = a->features % 8 == 0 && rows_vector(a->dtable, a->ldt, 4) && rows_vector(a->dout, a->ldo, es);
   DION_TRY(launch_status("k_embed_sum", a->dtype == DION_BF16   ? launch_sum<__nv_bfloat16>(p, al, g.segs, s)
                                         : a->dtype == DION_FP16 ? launch_sum<__half>(p, al, g.segs, s)
                                                                 : launch_sum<float>(p, al, g.segs, s)));

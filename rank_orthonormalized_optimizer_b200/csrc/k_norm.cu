@@ -853,7 +853,7 @@ dion_status norm_impl(const dion_norm* a, void* stream) {
   for (const auto& r : rows) {
     if (!r.need || a->tokens == 0) continue;
     DION_TRY(check_rows(r.name, r.p, r.ld, a->features, es));
-    al = al && rows_aligned16(r.p, r.ld, es);
+    al = al && rows_vector(r.p, r.ld, es);
   }
   for (const float* g : {a->pre_gain, a->post_gain, a->gate}) al = al && (!g || aligned_to(g, 16));
   int sms = 0;
@@ -904,14 +904,14 @@ dion_status norm_grad_impl(const dion_norm_grad* a, void* ws, size_t ws_bytes, v
   for (const auto& r : rows) {
     if (!r.need || a->tokens == 0) continue;
     DION_TRY(check_rows(r.name, r.p, r.ld, a->features, es));
-    al = al && rows_aligned16(r.p, r.ld, es);
+    al = al && rows_vector(r.p, r.ld, es);
   }
   for (const float* g : {a->pre_gain, a->post_gain, a->gate}) al = al && (!g || aligned_to(g, 16));
   const size_t need = dion_norm_backward_workspace(a->tokens, a->features);
   if (need && !ws) return set_error(DION_ERR_INVALID_ARG, "workspace is NULL");
   if (ws_bytes < need)
     return set_error(DION_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes, %zu needed", ws_bytes, need);
-  if (!aligned_to(ws, 16)) return set_error(DION_ERR_MISALIGNED, "workspace is not 16-byte aligned");
+  if (!aligned_to(ws, 32)) return set_error(DION_ERR_MISALIGNED, "workspace is not 32-byte aligned");
   int sms = 0;
   DION_TRY(check_sm100(&sms));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -102,6 +102,13 @@ __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
 }
+// A lane's 8 floats of its row, a whole 32-byte sector: the lanes of a warp write 32 rows, and
+// two 16-byte halves would reach L2 as two partial sectors.
+__device__ __forceinline__ void store_sector(float* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
 template <int R> __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
 }
@@ -483,8 +490,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
       if (t.part >= 0) {
         float* g = p.parts + ((int64_t)t.part * PM + rank * BM + row0 + place) * BN + col0;
 #pragma unroll
-        for (int i = 0; i < HB; i += 4)
-          *reinterpret_cast<float4*>(g + i) = make_float4(run[i], run[i + 1], run[i + 2], run[i + 3]);
+        for (int i = 0; i < HB; i += 8) store_sector(g + i, run + i);
       } else if (row >= p.m) {
         // a lane past the last feature writes nothing
       } else if (p.transposed) {
@@ -498,17 +504,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
       } else {
         float* g = p.out + row * p.ldg + n0;
 #pragma unroll
-        for (int i = 0; i < HB; i += 4) {
-          if (p.vec && n0 + i + 3 < p.n) {
-            float4 o = make_float4(run[i], run[i + 1], run[i + 2], run[i + 3]);
+        for (int i = 0; i < HB; i += 8) {
+          if (p.vec && n0 + i + 7 < p.n) {
             if (p.accumulate) {
-              const float4 a = *reinterpret_cast<const float4*>(g + i);
-              o.x += a.x; o.y += a.y; o.z += a.z; o.w += a.w;
+              const float4 a = *reinterpret_cast<const float4*>(g + i), b = *reinterpret_cast<const float4*>(g + i + 4);
+              run[i] += a.x; run[i + 1] += a.y; run[i + 2] += a.z; run[i + 3] += a.w;
+              run[i + 4] += b.x; run[i + 5] += b.y; run[i + 6] += b.z; run[i + 7] += b.w;
             }
-            *reinterpret_cast<float4*>(g + i) = o;
+            store_sector(g + i, run + i);
           } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 8; ++j)
               if (n0 + i + j < p.n) g[i + j] = run[i + j] + (p.accumulate ? g[i + j] : 0.f);
           }
         }
@@ -526,8 +532,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   }
 }
 
-// Adds the split tiles' partial sums in order, into G in either layout: 32 x 32 of a tile.
-__global__ void __launch_bounds__(256) k_wgrad_join(const WgradP p, int bn) {
+// Adds the split tiles' partial sums in order, into G in either layout: 32 x 32 of a tile, an
+// element a thread, so that a small matrix's few blocks have their loads in flight at once.
+__global__ void __launch_bounds__(1024) k_wgrad_join(const WgradP p, int bn) {
   __shared__ float block[32][33];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int tile = p.whole + blockIdx.z;
@@ -536,31 +543,24 @@ __global__ void __launch_bounds__(256) k_wgrad_join(const WgradP p, int bn) {
   if (row0 >= p.m || col0 >= p.n) return;
   grid_wait();
   const int64_t plane = (int64_t)PM * bn;
-  const float* from = p.parts + blockIdx.z * p.splits * plane + (int64_t)i0 * bn + j0;
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int s = 0; s < p.splits; ++s)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) sum[k] += from[s * plane + (ty + 8 * k) * bn + tx];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int64_t i = row0 + ty + 8 * k, j = col0 + tx;
-    if (!p.transposed && i < p.m && j < p.n) {
-      float* g = p.out + i * p.ldg + j;
-      *g = sum[k] + (p.accumulate ? *g : 0.f);
-    }
-    block[ty + 8 * k][tx] = sum[k];
+  const float* from = p.parts + blockIdx.z * p.splits * plane + (int64_t)(i0 + ty) * bn + j0 + tx;
+  float sum = 0.f;
+#pragma unroll 8
+  for (int s = 0; s < p.splits; ++s) sum += from[s * plane];
+  int64_t i = row0 + ty, j = col0 + tx;
+  if (!p.transposed) {
+    if (i >= p.m || j >= p.n) return;
+    float* g = p.out + i * p.ldg + j;
+    *g = sum + (p.accumulate ? *g : 0.f);
+    return;
   }
-  if (!p.transposed) return;
+  block[ty][tx] = sum;
   __syncthreads();
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int64_t j = col0 + ty + 8 * k, i = row0 + tx;
-    if (i < p.m && j < p.n) {
-      float* g = p.out + j * p.ldg + i;
-      *g = block[tx][ty + 8 * k] + (p.accumulate ? *g : 0.f);
-    }
-  }
+  i = row0 + tx;
+  j = col0 + ty;
+  if (i >= p.m || j >= p.n) return;
+  float* g = p.out + j * p.ldg + i;
+  *g = block[tx][ty] + (p.accumulate ? *g : 0.f);
 }
 
 // D into rows that a TMA map can take (a multiple of 8 columns, the rest zero).
@@ -739,13 +739,13 @@ dion_status one_grad(const dion_grad_source& src, int accumulate, char* ws, int3
   p.blocks_per_split = g.blocks_per_split;
   p.transposed = src.transposed != 0;
   p.accumulate = accumulate != 0;
-  p.vec = rows_aligned16(src.G, src.ldg, 4);
+  p.vec = aligned_to(src.G, 32) && src.ldg % 8 == 0;
   p.scale4 = p.ld_scale % 4 == 0 && aligned_to(p.scale, 4);
   p.max_spins = kMaxSpins;
   const dion_status st = g.bn == 256 ? launch<256>(mq, md, p, sms, s) : launch<128>(mq, md, p, sms, s);
   if (st != DION_OK || g.tail == 0) return st;
   return launch_status("k_wgrad_join", launch_after(k_wgrad_join, dim3((unsigned)(g.bn / 32), PM / 32, (unsigned)g.tail),
-                                                    256, 0, s, p, g.bn));
+                                                    1024, 0, s, p, g.bn));
 }
 
 dion_status wgrad_impl(const dion_grad_source* src, int32_t nsrc, int32_t accumulate, void* ws,
@@ -757,7 +757,7 @@ dion_status wgrad_impl(const dion_grad_source* src, int32_t nsrc, int32_t accumu
   if (need && !ws) return set_error(DION_ERR_INVALID_ARG, "workspace is NULL");
   if (ws_bytes < need)
     return set_error(DION_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes, %zu needed", ws_bytes, need);
-  if (!aligned_to(ws, 16)) return set_error(DION_ERR_MISALIGNED, "workspace is not 16-byte aligned");
+  if (need && !aligned_to(ws, 32)) return set_error(DION_ERR_MISALIGNED, "workspace is not 32-byte aligned");
   if (d_status && !aligned_to(d_status, 4))
     return set_error(DION_ERR_MISALIGNED, "d_status is not 4-byte aligned");
   int sms = 0;

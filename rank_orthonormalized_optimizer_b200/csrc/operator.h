@@ -64,6 +64,26 @@ inline bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintpt
 inline bool valid_dtype(int32_t t) { return t == DION_BF16 || t == DION_FP16 || t == DION_FP32; }
 inline int64_t dtype_bytes(int32_t t) { return t == DION_FP32 ? 4 : 2; }
 
+// Row of an item's index: a division by the items of a row.  In 32 bits (indexes below 2^31)
+// by a multiplication with the rounded-up reciprocal, after Granlund and Montgomery, "Division
+// by Invariant Integers using Multiplication": with s = ceil(log2 d) and
+// m = floor(2^32 (2^s - d) / d) + 1, i / d = (mulhi(m, i) + i) >> s.
+template <typename I> struct RowDiv;
+template <> struct RowDiv<uint32_t> {
+  uint32_t m, s;
+  explicit RowDiv(int64_t d) {
+    s = 0;
+    while ((int64_t(1) << s) < d) ++s;
+    m = (uint32_t)(((uint64_t)((int64_t(1) << s) - d) << 32) / (uint64_t)d + 1);
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t i) const { return (__umulhi(m, i) + i) >> s; }
+};
+template <> struct RowDiv<int64_t> {
+  int64_t d;
+  explicit RowDiv(int64_t n) : d(n) {}
+  __device__ __forceinline__ int64_t operator()(int64_t i) const { return i / d; }
+};
+
 // Largest sizes taken: a grid's x dimension holds a row of each, and every offset
 // tokens * ld stays far below 2^63.
 constexpr int64_t kMaxTokens = INT32_MAX;
@@ -91,6 +111,11 @@ inline dion_status check_rows(const char* name, const void* p, int64_t ld, int64
 // Whether every row of the array starts on a 16-byte boundary.
 inline bool rows_aligned16(const void* p, int64_t ld, int64_t elem) {
   return aligned_to(p, 16) && (ld * elem) % 16 == 0;
+}
+
+// Whether every row can be moved 8 elements at a time (rows.cuh): 16 bytes, 32 of fp32.
+inline bool rows_vector(const void* p, int64_t ld, int64_t elem) {
+  return aligned_to(p, 8 * (size_t)elem) && ld % 8 == 0;
 }
 
 // Rows of the 8-bit form: features rounded up to whole blocks.

@@ -22,8 +22,9 @@ template <> __device__ __forceinline__ float from_float<float>(float v) { return
 template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half from_float<__half>(float v) { return __float2half_rn(v); }
 
-// Raw bits of 8 consecutive elements (16 bytes for the 2-byte types, 32 for fp32); the
-// pointer is 16-byte aligned.  Loaded past L1, where the gains of a norm stay instead.
+// Raw bits of 8 consecutive elements (16 bytes for the 2-byte types, 32 for fp32, moved at
+// once: in two 16-byte halves each access of a warp would touch half of every sector); the
+// pointer is aligned to them.  Loaded past L1, where the gains of a norm stay instead.
 template <typename T> struct Raw8 { uint4 a; };
 template <> struct Raw8<float> { uint4 a, b; };
 
@@ -33,11 +34,23 @@ __device__ __forceinline__ uint4 ld_stream(const void* p) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
   return v;
 }
+__device__ __forceinline__ void ld_stream32(const void* p, uint4& a, uint4& b) {
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+               : "l"(p) : "memory");
+}
+__device__ __forceinline__ void st_vec32(void* p, uint4 a, uint4 b) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
+               "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
 __device__ __forceinline__ void st_vec(void* p, uint4 v) { *reinterpret_cast<uint4*>(p) = v; }
 
 template <typename T> __device__ __forceinline__ Raw8<T> load_raw(const T* p) { return {ld_stream(p)}; }
 template <> __device__ __forceinline__ Raw8<float> load_raw<float>(const float* p) {
-  return {ld_stream(p), ld_stream(p + 4)};
+  Raw8<float> r;
+  ld_stream32(p, r.a, r.b);
+  return r;
 }
 template <typename T> __device__ __forceinline__ Raw8<T> zero_raw() { return {make_uint4(0, 0, 0, 0)}; }
 template <> __device__ __forceinline__ Raw8<float> zero_raw<float>() {
@@ -69,27 +82,29 @@ __device__ __forceinline__ void unpack(const Raw8<__half>& r, float* v) {
 }
 
 __device__ __forceinline__ void store8(float* p, const float* v) {
-  st_vec(p, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
-  st_vec(p + 4, make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])));
+  st_vec32(p, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])),
+           make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])));
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) {
+__device__ __forceinline__ uint4 pack8(const float* v, __nv_bfloat16) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
     w[i] = *reinterpret_cast<const uint32_t*>(&b);
   }
-  st_vec(p, make_uint4(w[0], w[1], w[2], w[3]));
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void store8(__half* p, const float* v) {
+__device__ __forceinline__ uint4 pack8(const float* v, __half) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const __half2 b = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
     w[i] = *reinterpret_cast<const uint32_t*>(&b);
   }
-  st_vec(p, make_uint4(w[0], w[1], w[2], w[3]));
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) { st_vec(p, pack8(v, __nv_bfloat16())); }
+__device__ __forceinline__ void store8(__half* p, const float* v) { st_vec(p, pack8(v, __half())); }
 
 // ---- 8-bit form: a block of 32 features x_i is e4m3(x_i 2^-e) and the byte e + 127, e the
 // smallest exponent with max|x_i| <= 448 2^e (448 = 1.75 2^8 is e4m3's largest value, so
@@ -101,6 +116,22 @@ constexpr uint32_t kInfBits = 0x7f800000u;
 
 // max over the block of the magnitudes' bits (they order as the values do, NaN on top)
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// the same over 8 values as they are stored: 16-bit magnitudes order by their bits, too
+__device__ __forceinline__ uint32_t abs_bits8(const Raw8<float>& r) {
+  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, w[i] & 0x7fffffffu);
+  return top;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t abs_bits8(const Raw8<T>& r) {
+  constexpr uint32_t M = 0x7fff7fffu;
+  const uint32_t two = __vmaxu2(__vmaxu2(r.a.x & M, r.a.y & M), __vmaxu2(r.a.z & M, r.a.w & M));
+  const uint16_t one = (uint16_t)max(two & 0xffffu, two >> 16);
+  return __float_as_uint(to_float(*reinterpret_cast<const T*>(&one)));
+}
 
 __device__ __forceinline__ int act_exponent(uint32_t top) {
   const int e = (int)(top >> 23) - 127 - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
