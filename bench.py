@@ -649,6 +649,98 @@ def run_vector_only(args):
         dist.destroy_process_group()
 
 
+# ------------------------------------------------------------ where gradients come from
+def gradient_calls(gw, dev):
+    """{name: (call, bytes, flops)} of one layer's operators on synthetic rows, and the step
+    that reads what they wrote.  Bytes and flops are what the call cannot do without."""
+    import torch
+
+    from rank_orthonormalized_optimizer_b200 import (ActCheckpoint, DionB200, EmbedGradPlan,
+                                                     EmbedPlan, NormGradPlan, NormPlan, SavedStep,
+                                                     VecStepPlan, WeightGradPlan)
+    t, d, f, v = gw.tokens, gw.hidden, gw.ff, gw.vocab
+    i = W.gradient_inputs(gw, dev)
+    rows = lambda w=d: torch.empty(t, w, dtype=torch.bfloat16, device=dev)  # noqa: E731
+    x, h, u, dx, dy = (rows() for _ in range(5))
+    kept = ActCheckpoint(t, d, device=dev)
+    gains = {k: i[k] for k in ("pre_gain", "post_gain", "gate")}
+    grads = {"d" + k: torch.empty(d, device=dev) for k in gains}
+    dtable = torch.empty(v, d, device=dev)
+    shapes = [(1, d, d, gw.rank), (1, d, f, gw.rank)]
+    G = [torch.empty(c, m, n, device=dev) for c, m, n, _ in shapes]
+    lookup = EmbedPlan(i["table"], i["ids"], x, scale=d ** 0.5)
+    norm = NormPlan(x, i["y"], h=h, u=u, checkpoint=kept, residual_scale=0.5, **gains)
+    norm_grad = NormGradPlan(h, i["y"], du=i["du"], dh=i["dh"], dx=dx, dy=dy, residual_scale=0.5,
+                             **gains, **grads)
+    w_attn = WeightGradPlan([kept], [i["d_attn"]], [G[0][0]])
+    w_mlp = WeightGradPlan([kept], [i["d_mlp"]], [G[1][0]])
+    embed_grad = EmbedGradPlan(i["ids"], dx, dtable, scale=d ** 0.5)
+    opt = DionB200(shapes)
+    X = [torch.randn_like(g) for g in G]
+    M = [torch.zeros_like(g) for g in G]
+    Q = [torch.nn.functional.normalize(torch.randn(1, n, r, device=dev), dim=1)
+         for _, _, n, r in shapes]
+    step = SavedStep(opt, [kept, kept], [i["d_attn"], i["d_mlp"]])
+    vec = list(gains.values()) + [i["table"].view(-1)]
+    vstep = VecStepPlan(vec, list(grads.values()) + [dtable.view(-1)],
+                        *([torch.zeros_like(p) for p in vec] for _ in range(2)))
+    row, kept_row = 2 * t * d, t * d * 33 / 32
+    met = int(i["ids"][i["ids"] >= 0].unique().numel())     # rows of the table that are read
+    return {
+        "lookup": (lookup.lookup, 8 * t + 4 * met * d + row, t * d),
+        "norm_keep": (norm.forward, 4 * row + kept_row, 12 * t * d),
+        "act_save": (lambda: kept.save(u), row + kept_row, 4 * t * d),
+        "act_load": (lambda: kept.load(u), row + kept_row, t * d),
+        "norm_backward": (norm_grad.backward, 6 * row, 24 * t * d),
+        "weight_grad_attn": (w_attn.backward, kept_row + row + 4 * d * d, 2 * t * d * d),
+        "weight_grad_mlp": (w_mlp.backward, kept_row + 2 * t * f + 4 * d * f, 2 * t * d * f),
+        "embed_backward": (embed_grad.backward, 8 * t + row + 4 * v * d, 2 * t * d),
+        "step_from_saved": (lambda: step.step(X, M, G, Q, gw.lr),
+                            2 * kept_row + row + 2 * t * f + 24 * d * (d + f),
+                            2 * t * d * (d + f) + 8 * d * (d + f) * gw.rank),
+        "vector_step": (lambda: vstep.step(1), 28 * sum(p.numel() for p in vec), 0),
+    }
+
+
+def run_gradients_only(args):
+    """The operators that give the step its gradients: one JSON line with their timings."""
+    import torch
+
+    rank, world = dist_setup("nccl")
+    _, _, local = dist_env()
+    torch.cuda.set_device(local)
+    dev = torch.device("cuda", local)
+    peaks = measured_peaks()
+    gw = W.GRADIENT_WORKLOADS[args.gradients_only]
+    rec = {}
+    flush = torch.empty(2 * L2_BYTES, dtype=torch.uint8, device=dev)
+    for name, (call, nbytes, flops) in gradient_calls(gw, dev).items():
+        for _ in range(args.warmup):
+            call()
+        pairs = []
+        for _ in range(args.steps):
+            flush.zero_()                 # every call starts with its inputs out of L2
+            e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+            e[0].record()
+            call()
+            e[1].record()
+            pairs.append(e)
+        torch.cuda.synchronize(dev)
+        us = max_over_ranks(statistics.median(a.elapsed_time(b) for a, b in pairs), dev) * 1e3
+        floor = max(nbytes / peaks["hbm_gbs"] / 1e3, flops / peaks["bf16_tflops"] / 1e6)
+        rec[name] = {"us": us, "GBs": nbytes / us / 1e3, "TFLOPs": flops / us / 1e6,
+                     "floor_us": floor, "frac_of_floor": floor / us}
+    if rank == 0:
+        print(json.dumps({"metric": "gradient operators", "n_gpus": world, "steps": args.steps,
+                          "warmup": args.warmup, "data": "synthetic",
+                          "config": {"workload": gw.name, "l2": "flushed before every call"},
+                          "peak_GBs": peaks["hbm_gbs"], "peak_TFLOPs": peaks["bf16_tflops"],
+                          "peak_source": peaks["source"], "gradients": rec}), flush=True)
+    import torch.distributed as dist
+    if dist.is_initialized():
+        dist.destroy_process_group()
+
+
 # ------------------------------------------------------------------ the oracle arm
 def run_reference(args):
     rank, world, _ = dist_env()
@@ -705,6 +797,9 @@ def main(argv=None):
     ap.add_argument("--vector-only", default=None, choices=sorted(W.VECTOR_WORKLOADS),
                     help="time only the vector-parameter step on this workload (for profiling "
                          "its kernel with little else on the device)")
+    ap.add_argument("--gradients-only", default=None, choices=sorted(W.GRADIENT_WORKLOADS),
+                    help="time only the operators that give the step its gradients (norm, 8-bit "
+                         "activations, weight gradient, embedding) on this workload")
     args = ap.parse_args(argv)
     if args.warmup < 3 and args.impl == "ours":
         print("warning: fewer than 3 warm-up steps", file=sys.stderr)
@@ -712,6 +807,8 @@ def main(argv=None):
         run_reference(args)
     elif args.vector_only:
         run_vector_only(args)
+    elif args.gradients_only:
+        run_gradients_only(args)
     elif args.rowshard:
         run_rowshard(args)
     else:

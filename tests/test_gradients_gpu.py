@@ -625,6 +625,75 @@ def test_two_streams_with_their_own_workspaces():
     assert torch.equal(Ga, want[0]) and torch.equal(Gb, want[1])
 
 
+def test_offsets_past_32_bits():
+    """40 rows 2^26 elements apart (5.4 GB of bf16): the last rows lie past 2^31 elements."""
+    t, d, ld = 40, 64, 1 << 26
+    far = torch.empty(t * ld, dtype=torch.bfloat16, device="cuda").view(t, ld)
+    x = far[:, :d]
+    vals = torch.randn(t, d, generator=_gen(1)).bfloat16()
+    x.copy_(vals.cuda())
+    kept, near = dion.ActCheckpoint(t, d), dion.ActCheckpoint(t, d)
+    kept.save(x)
+    near.save(vals.cuda())
+    assert torch.equal(kept.q, near.q) and torch.equal(kept.scale, near.scale)
+    # the norm, rows to rows of the same buffer; and backwards into it
+    u, want = far[:, d:2 * d], torch.empty(t, d, dtype=torch.bfloat16, device="cuda")
+    dion.NormPlan(x, u=u).forward()
+    dion.NormPlan(vals.cuda(), u=want).forward()
+    assert torch.equal(u, want)
+    dx = far[:, 2 * d:3 * d]
+    dion.NormGradPlan(x, du=u, dx=dx).backward()
+    dw = torch.empty_like(want)
+    dion.NormGradPlan(vals.cuda(), du=want, dx=dw).backward()
+    assert torch.equal(dx, dw)
+    # the far rows as a table, as dY, as the gradient of looked-up rows
+    ids = torch.tensor([t - 1, 0, -1, t - 2, t - 1], device="cuda")
+    out = far[:5, 3 * d:4 * d]
+    dion.EmbedPlan(x, ids, out).lookup()
+    assert torch.equal(out[0], x[t - 1]) and torch.equal(out[3], x[t - 2]) and not out[2].any()
+    g, gw = torch.empty(t, d, device="cuda"), torch.empty(t, d, device="cuda")
+    dion.EmbedGradPlan(torch.arange(t, device="cuda"), x, g).backward()
+    assert torch.equal(g, x.float())
+    G, Gw = torch.empty(d, d, device="cuda"), torch.empty(d, d, device="cuda")
+    dion.WeightGradPlan([kept], [x], [G]).backward()
+    dion.WeightGradPlan([kept], [vals.cuda()], [Gw]).backward()
+    assert torch.equal(G, Gw)
+    del far, x, u, dx, out
+    # a table and G of far rows in fp32 (10.7 GB)
+    far = torch.full((t * ld,), 7.0, device="cuda").view(t, ld)
+    dion.EmbedGradPlan(torch.arange(t - 1, -1, -1, device="cuda"), vals.cuda(), far[:, :d]).backward()
+    assert torch.equal(far[:, :d], vals.cuda().float().flip(0)) and bool((far[:, d] == 7.0).all())
+    dion.WeightGradPlan([kept], [vals.cuda()[:, :t].contiguous()], [far[:, :d]], transposed=True).backward()
+    ref = torch.empty(t, d, device="cuda")
+    dion.WeightGradPlan([kept], [vals.cuda()[:, :t].contiguous()], [ref], transposed=True).backward()
+    assert torch.equal(far[:, :d], ref)
+
+
+def test_a_plan_of_another_device_is_refused(monkeypatch):
+    x = torch.zeros(4, 64, device="cuda")
+    plan, kept = dion.NormPlan(x, u=torch.empty_like(x)), dion.ActCheckpoint(4, 64)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: x.device.index + 1)
+    with pytest.raises(ValueError, match="current device"):
+        plan.forward()
+    with pytest.raises(ValueError, match="current device"):
+        kept.save(x)
+
+
+def test_two_lists_of_ids_in_turn_with_one_workspace():
+    """Calls that follow each other on a stream may share a workspace: what one leaves there
+    (sorted ids, the list of runs to join) does not reach the next."""
+    v, d = 50, 264
+    ws = torch.empty(1 << 22, dtype=torch.uint8, device="cuda").fill_(255)
+    for seed, t in ((1, 2000), (2, 3), (3, 700), (4, 2000)):
+        ids = _ids("few", t, v, seed)
+        dout = torch.randn(t, d, generator=_gen(seed)).cuda()
+        g = torch.empty(v, d, device="cuda")
+        dion.EmbedGradPlan(ids.cuda(), dout, g, workspace=ws).backward()
+        mag = go.embed_grad(ids.numpy(), np.abs(_np(dout)), v)
+        hits = np.bincount(ids.numpy(), minlength=v)
+        assert np.all(np.abs(_np(g) - go.embed_grad(ids.numpy(), _np(dout), v)) <= (hits[:, None] + 2) * U * mag)
+
+
 def test_plans_refuse_tensors_that_do_not_fit():
     x = torch.zeros(4, 64, device="cuda")
     with pytest.raises(ValueError, match="must be"):

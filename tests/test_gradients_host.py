@@ -283,3 +283,29 @@ def test_plans_check_their_tensors_on_the_host():
     for bad in (torch.zeros(8), None):
         with pytest.raises(ValueError):
             dion.NormPlan(bad)
+
+
+def test_c99_caller(tmp_path):
+    import os
+    import shutil
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    exe, libdir = tmp_path / "abi_gradients", os.path.dirname(dion.LIB_PATH)
+    subprocess.run([cc, "-std=c99", "-Wall", "-Werror", "-pedantic", "-I",
+                    os.path.join(root, "include"), os.path.join(root, "tests", "c", "abi_gradients.c"),
+                    "-L", libdir, "-ldion_b200", f"-Wl,-rpath,{libdir}", "-o", str(exe)],
+                   check=True, capture_output=True, text=True)
+    out = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert out.returncode == 0 and out.stdout.strip() == "ok", out.stdout + out.stderr
+
+
+def test_gradient_workloads_are_seeded():
+    import torch
+    import workloads as W
+    gw = W.GRADIENT_WORKLOADS["layer_h256_ff128_t300"]
+    a, b, c = W.gradient_inputs(gw), W.gradient_inputs(gw), W.gradient_inputs(gw, step=1)
+    assert all(torch.equal(a[k], b[k]) for k in a) and not torch.equal(a["y"], c["y"])
+    assert a["ids"].min() == -1 and a["ids"].max() < gw.vocab and a["d_mlp"].shape == (300, 128)

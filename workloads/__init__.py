@@ -18,6 +18,7 @@ large ones; a test always copies the same drawn tensor to both sides.
 from __future__ import annotations
 
 import hashlib
+import math
 from dataclasses import dataclass, field
 
 import torch
@@ -117,7 +118,9 @@ WORKLOADS = {
 #: the workload a throughput figure is quoted on (7B-like transformer shapes)
 HEADLINE = "transformer_h4096_l32_ff11008_r256"
 
-_KINDS = {"X": 1, "Q": 2, "G": 3, "U": 4, "V": 5, "M": 6, "S": 7}
+_KINDS = {"X": 1, "Q": 2, "G": 3, "U": 4, "V": 5, "M": 6, "S": 7, "ids": 8, "table": 9,
+          "pre_gain": 10, "post_gain": 11, "gate": 12, "y": 13, "du": 14, "dh": 15, "d_attn": 16,
+          "d_mlp": 17}
 
 
 def seed_for(workload: str, bucket: int, slot: int, kind: str, step: int = 0) -> int:
@@ -259,3 +262,51 @@ def vector_state(vw: VectorWorkload, i: int, step: int = 0, device="cpu"):
     m = _randn((n,), seed_for(vw.name, i, 0, "M"), device) * 1e-3
     v = (_randn((n,), seed_for(vw.name, i, 0, "S"), device) * 1e-3) ** 2
     return x, g, m, v
+
+
+# ------------------------------------------------------------ where gradients come from
+@dataclass(frozen=True)
+class GradientWorkload:
+    """One layer's share of a training step: ids looked up in a table, the norms around a
+    block, the block's inputs kept in 8 bits, and the gradients of a hidden x hidden and a
+    hidden x ff weight, the gains and the table."""
+    name: str
+    tokens: int
+    hidden: int
+    ff: int
+    vocab: int
+    rank: int
+    lr: float = 0.01
+
+
+GRADIENT_WORKLOADS = {
+    # the shapes of the 7B-like decoder's attention and MLP weights, 16384 tokens
+    "layer_h4096_ff11008_t16384": GradientWorkload("layer_h4096_ff11008_t16384", 16384, 4096,
+                                                   11008, 32768, 256),
+    # the 1.3B-like decoder's
+    "layer_h2048_ff8192_t8192": GradientWorkload("layer_h2048_ff8192_t8192", 8192, 2048, 8192,
+                                                 32768, 256),
+    # seconds on a CPU oracle
+    "layer_h256_ff128_t300": GradientWorkload("layer_h256_ff128_t300", 300, 256, 128, 96, 32),
+}
+
+
+def gradient_inputs(gw: GradientWorkload, device="cpu", step: int = 0) -> dict:
+    """Synthetic tensors of one layer: table ~ 0.02 N(0, 1), word-like id frequencies (about
+    1 / rank) with the last 2 % padded by -1, block outputs y ~ N(0, 1), gains 1 + 0.1 N(0, 1),
+    gradients 1e-3 N(0, 1); rows bf16, parameters fp32."""
+    def r(kind, *shape):
+        return _randn(shape, seed_for(gw.name, 0, 0, kind, step), device)
+
+    t, d = gw.tokens, gw.hidden
+    u = torch.rand(t, generator=torch.Generator().manual_seed(seed_for(gw.name, 0, 0, "ids", step)),
+                   dtype=torch.float64)
+    ids = (torch.exp(u * math.log(gw.vocab + 1)).floor().long() - 1).clamp_(0, gw.vocab - 1)
+    ids[t - t // 50:] = -1
+    out = {"ids": ids.to(device), "table": 0.02 * r("table", gw.vocab, d)}
+    for k in ("pre_gain", "post_gain", "gate"):
+        out[k] = 1 + 0.1 * r(k, d)
+    out["y"] = r("y", t, d).bfloat16()
+    for k, w in (("du", d), ("dh", d), ("d_attn", d), ("d_mlp", gw.ff)):
+        out[k] = (1e-3 * r(k, t, w)).bfloat16()
+    return out
