@@ -38,7 +38,7 @@ constexpr int kSmemMost = 226 * 1024;    // of the rings of one SM's CTAs
 
 // Threads of a CTA, and CTAs of a streaming grid on an SM (512 threads of 128 registers).
 constexpr int cta_threads(int nt) { return nt == 32 ? 32 * kWarpRows : nt; }
-constexpr int ctas_per_sm(int nt) { return 512 / cta_threads(nt); }
+constexpr int ctas_per_sm(int nt) { return cta_threads(nt) > 512 ? 1 : 512 / cta_threads(nt); }
 
 struct NormP {
   const void *x, *y;

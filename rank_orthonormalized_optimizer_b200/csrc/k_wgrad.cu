@@ -19,7 +19,9 @@
 //   warps 16..23  epilogue
 // The tensor cores' accumulation rounds toward zero, which adds up over thousands of MMAs,
 // so the tokens are cut into chunks of kChunk blocks, each accumulated from zero in TMEM
-// (two accumulators in turn), and the epilogue warps add the chunks in fp32 registers.
+// (two accumulators in turn), and the epilogue warps add the chunks in fp32 registers: over
+// 16384 like-signed products 3e-7 off (an fp32 product on CUDA cores 6e-7), at 1227 us for
+// m = 4096, n = 11008; chunks of 8 blocks 1.3e-7 at 1258 us, of 4 8e-8 at 1319 us.
 // The tiles that do not fill a last round over all pairs (all of them, in a small matrix) are
 // also split over the tokens, so that every pair has a share; their partial sums go to the
 // workspace and a second kernel adds them in order.  Every wait is bounded.
@@ -40,7 +42,7 @@ using namespace tc;
 constexpr int BM = 128;      // features of A per CTA = TMEM lanes
 constexpr int PM = 2 * BM;   // features of a pair's tile
 constexpr int BK = 64;       // tokens per stage
-constexpr int kChunk = 8;    // stages per accumulation chunk
+constexpr int kChunk = 16;   // stages per accumulation chunk
 constexpr int NT = 32 * (4 + 12 + 8);
 constexpr int SQ = 6;        // stages of the 8-bit tiles
 constexpr int SB = 6;        // stages of the D tiles

@@ -86,12 +86,22 @@ EXPORTED = ["dion_act_save", "dion_act_load", "dion_weight_grad_workspace", "dio
             "dion_embed_backward_workspace", "dion_embed_backward"]
 
 
+_CODES = {}     # torch dtype -> dion_dtype; filled on first use (torch is imported lazily)
+
+
+def _dtype_codes() -> dict:
+    if not _CODES:
+        import torch
+        _CODES.update({torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16,
+                       torch.float32: DTYPE_FP32})
+    return _CODES
+
+
 def _dtype(t) -> int:
-    import torch
-    code = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32}
-    if t.dtype not in code:
+    code = _dtype_codes().get(t.dtype)
+    if code is None:
         raise ValueError(f"bf16, fp16 or fp32 expected, got {t.dtype}")
-    return code[t.dtype]
+    return code
 
 
 class _Bound:
@@ -181,24 +191,33 @@ class ActCheckpoint(_Bound):
                 raise ValueError(f"{name} must be contiguous {shape}, got {tuple(t.shape)}")
         self.q, self.scale = q, scale
         self.args = ActKept(q.data_ptr(), scale.data_ptr(), self.tokens, self.features)
-        self._keep = [q, scale]
+        self._keep, self._shape = [q, scale], (self.tokens, self.features)
+        self._ref = ctypes.byref(self.args)
+        _dtype_codes()
 
     def _arg(self, name, x):
         """x's pointer, row stride and type; x itself is the caller's to keep."""
-        ptr, ld = self._rows(name, x, (self.tokens, self.features))
+        import torch
+        # the usual case in a few comparisons: this is a call a layer, not a plan
+        code = _CODES.get(x.dtype) if isinstance(x, torch.Tensor) else None
+        if code is not None and x.device == self._device and x.shape == self._shape:
+            ld, one = x.stride()
+            if one == 1 and ld >= self.features:
+                return x.data_ptr(), ld, code
+        ptr, ld = self._rows(name, x, self._shape)
         self._keep.pop()
-        return c_void_p(ptr), ld, _dtype(x)
+        return ptr, ld, _dtype(x)
 
     def save(self, x, stream=None):
         """Keep x [tokens, features] (bf16, fp16 or fp32)."""
         ptr, ld, ty = self._arg("x", x)
-        _check(dion_act_save(ptr, ld, ty, ctypes.byref(self.args), self._stream(stream)),
+        _check(dion_act_save(ptr, ld, ty, self._ref, self._stream(stream)),
                "dion_act_save")
 
     def load(self, out, stream=None):
         """Write what was kept into out [tokens, features] (bf16, fp16 or fp32)."""
         ptr, ld, ty = self._arg("out", out)
-        _check(dion_act_load(ctypes.byref(self.args), ptr, ld, ty, self._stream(stream)),
+        _check(dion_act_load(self._ref, ptr, ld, ty, self._stream(stream)),
                "dion_act_load")
         return out
 

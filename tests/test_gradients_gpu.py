@@ -11,9 +11,10 @@ norm: a row sum runs over at most 32 terms in a thread, 5 shuffles and 16 warps,
   over T rows adds T / 148 + 60 terms one after the other: below 2^-16 of the absolute sum for
   T <= 10^4 (the gradient A itself is off by 2^-17).
 act: exact (the same rounding rule): values must be equal.
-weight_grad: products are exact; a chunk of 256 tokens takes 16 tensor-core additions of at
-  most 2^-22 of the absolute sum each, the chunks are added in fp32: 2^-18 + (T / 256 + 8) u
-  of sum |a| |d|.
+weight_grad: products are exact; a chunk of 1024 tokens takes 64 tensor-core additions, each
+  cut off by at most 2^-23 of the running absolute sum, which grows from nothing to the
+  chunk's: 64 * 2^-23 / 2 = 2^-18 of it; the chunks and splits are added in fp32:
+  2^-18 + (T / 256 + 8) u of sum |a| |d|.
 embedding: lookup half |out| + u |out|; the gradient of a token met k times
   (k + 2) u of scale * sum |dout|.
 A stored fp16 value below its smallest normal is off by up to 2^-25.
