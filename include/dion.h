@@ -446,7 +446,8 @@ int32_t dion_vec_last_launch_count(void);
  * is read (fp32), next to the forward passes that they belong to.  Common to all:
  *  - arrays [tokens, features] are row-major with rows `ld*` elements apart (ld >=
  *    features); rows that start on 16 bytes with features % 8 == 0 take a vectorised
- *    path.  Rows past `tokens` and columns past `features` are neither read nor written.
+ *    path.  Rows past `tokens` are neither read nor written, columns past `features` are not
+ *    written (elements between rows may be loaded with their neighbours; they change nothing).
  *  - tokens may be 0.  Gains and gradients of gains are contiguous fp32 arrays.
  *  - arguments are checked before anything is enqueued; the work is enqueued on `stream`
  *    of the current device, and the call returns.  No entry point allocates device memory

@@ -16,6 +16,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;
+constexpr int kBlocks = 8;  // blocks of a warp in flight, in the form without vectors
 
 struct ActP {
   const void* x;   // save: source; load: destination (cast)
@@ -87,15 +88,25 @@ __global__ void __launch_bounds__(kThreads) k_act_save_any(const ActP p, const R
   const I per_row = (I)(p.ld / 32), total = (I)(p.tokens * per_row);
   const T* x = static_cast<const T*>(p.x);
   const int lane = threadIdx.x & 31;
-  for (I b = ((I)blockIdx.x * kThreads + threadIdx.x) / 32; b < total; b += (I)gridDim.x * kThreads / 32) {
-    const I r = row_of(b);
-    const int64_t row = r, col = (int64_t)(b - r * per_row) * 32 + lane;
-    const float v = col < p.features ? to_float(x[row * p.ldx + col]) : 0.f;
-    const uint32_t top = __reduce_max_sync(0xffffffffu, abs_bits(v));
-    const int e = act_exponent(top);
-    const bool fine = top < kInfBits;
-    p.q[row * p.ld + col] = fine ? (uint8_t)e4m3x2(v * act_unscale(e), 0.f) : 0;
-    if (lane == 0) p.scale[b] = fine ? e + 127 : 255;
+  const I stride = (I)gridDim.x * (kThreads / 32);
+  for (I b0 = (I)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; b0 < total; b0 += stride * kBlocks) {
+    float v[kBlocks];
+#pragma unroll
+    for (int u = 0; u < kBlocks; ++u) {
+      const I b = b0 + u * stride, r = row_of(b);
+      const int64_t col = (int64_t)(b - r * per_row) * 32 + lane;
+      v[u] = b < total && col < p.features ? to_float(x[(int64_t)r * p.ldx + col]) : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < kBlocks; ++u) {
+      const I b = b0 + u * stride;
+      if (b >= total) break;
+      const uint32_t top = __reduce_max_sync(0xffffffffu, abs_bits(v[u]));
+      const int e = act_exponent(top);
+      const bool fine = top < kInfBits;
+      p.q[(int64_t)b * 32 + lane] = fine ? (uint8_t)e4m3x2(v[u] * act_unscale(e), 0.f) : 0;
+      if (lane == 0) p.scale[b] = fine ? e + 127 : 255;
+    }
   }
 }
 
@@ -151,12 +162,22 @@ __global__ void __launch_bounds__(kThreads) k_act_load_any(const ActP p, const R
   const I per_row = (I)(p.ld / 32), total = (I)(p.tokens * per_row);
   T* x = static_cast<T*>(const_cast<void*>(p.x));
   const int lane = threadIdx.x & 31;
-  for (I b = ((I)blockIdx.x * kThreads + threadIdx.x) / 32; b < total; b += (I)gridDim.x * kThreads / 32) {
-    const I r = row_of(b);
-    const int64_t row = r, col = (int64_t)(b - r * per_row) * 32 + lane;
-    if (col < p.features)
-      x[row * p.ldx + col] =
-          from_float<T>(e4m3x2_float(p.q[row * p.ld + col]).x * act_scale(p.scale[b]));
+  const I stride = (I)gridDim.x * (kThreads / 32);
+  for (I b0 = (I)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; b0 < total; b0 += stride * kBlocks) {
+    uint32_t q[kBlocks], E[kBlocks];
+#pragma unroll
+    for (int u = 0; u < kBlocks; ++u) {
+      const I b = b0 + u * stride;
+      q[u] = b < total ? p.q[(int64_t)b * 32 + lane] : 0;
+      E[u] = b < total ? p.scale[b] : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < kBlocks; ++u) {
+      const I b = b0 + u * stride, r = row_of(b);
+      const int64_t col = (int64_t)(b - r * per_row) * 32 + lane;
+      if (b < total && col < p.features)
+        x[(int64_t)r * p.ldx + col] = from_float<T>(e4m3x2_float(q[u]).x * act_scale(E[u]));
+    }
   }
 }
 
@@ -175,13 +196,13 @@ void launch_as(const ActP& p, bool save, unsigned grid, cudaStream_t s) {
 // H pieces of 8 elements to a thread; 0: the form without vectors.
 template <typename T, int H>
 void launch(const ActP& p, bool save, int sms, cudaStream_t s) {
-  const int64_t items = p.tokens * (H > 0 ? p.ld / (8 * H) : p.ld);  // a thread's each
-  const int64_t cap = (int64_t)sms * (H > 0 ? 8 : 32);
-  const int64_t per_cta = H > 0 ? kThreads * kUnroll : kThreads;
+  const int64_t items = p.tokens * (H > 0 ? p.ld / (8 * H) : p.ld / 32);  // a thread's, or a warp's
+  const int64_t cap = (int64_t)sms * 8;
+  const int64_t per_cta = H > 0 ? kThreads * kUnroll : kThreads / 32;
   const unsigned grid = (unsigned)std::min((items + per_cta - 1) / per_cta, cap);
   // indexes in 32 bits where all of them fit (a loop's last step overshoots by its stride):
   // the division by the row length is what costs
-  if (items + cap * kThreads * kUnroll < (int64_t(1) << 31)) launch_as<T, uint32_t, H>(p, save, grid, s);
+  if (items + cap * kThreads * kBlocks < (int64_t(1) << 31)) launch_as<T, uint32_t, H>(p, save, grid, s);
   else launch_as<T, int64_t, H>(p, save, grid, s);
 }
 

@@ -423,22 +423,19 @@ __device__ __forceinline__ void write_zeros(const GradP& p, int64_t first) {
   __syncthreads();
   for (int64_t i = range[0] + threadIdx.x; i < range[1]; i += NT) met[p.key[i] - first] = 1;
   __syncthreads();
-  if (p.vec_table && p.features >= 4 * NT) {  // a row at a time
-    for (int r = 0; r < rows; ++r) {
-      if (met[r]) continue;
-      float4* to = reinterpret_cast<float4*>(p.dtable + (first + r) * p.ldt);
-      for (int64_t c = threadIdx.x; c < p.features / 4; c += NT) to[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    return;
-  }
-  const uint32_t step = p.vec_table ? 4 : 1, per_row = (uint32_t)(p.features / step);
-  const uint32_t total = rows * per_row;  // zero_rows * features < 2^31
-  for (uint32_t i = threadIdx.x; i < total; i += NT) {
-    const uint32_t r = i / per_row;
+  // a row at a time, by a warp or by the whole CTA: single elements up to a 16-byte boundary,
+  // vectors, and single elements to the end
+  const int group = p.features >= 4 * NT ? NT : 32, l = threadIdx.x % group;
+  for (int r = threadIdx.x / group; r < rows; r += NT / group) {
     if (met[r]) continue;
-    float* to = p.dtable + (first + r) * p.ldt + (i - r * per_row) * step;
-    if (p.vec_table) *reinterpret_cast<float4*>(to) = make_float4(0.f, 0.f, 0.f, 0.f);
-    else *to = 0.f;
+    float* row = p.dtable + (first + r) * p.ldt;
+    const int64_t head = min(p.features, (int64_t)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / 4);
+    const int64_t body = (p.features - head) / 4;
+    float4* to = reinterpret_cast<float4*>(row + head);
+    if (l < head) row[l] = 0.f;
+    for (int64_t c = l; c < body; c += group) to[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int64_t tail = head + body * 4 + l;
+    if (tail < p.features) row[tail] = 0.f;
   }
 }
 

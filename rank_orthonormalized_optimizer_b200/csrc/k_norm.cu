@@ -185,6 +185,29 @@ __device__ __forceinline__ void keep8(uint8_t* q, uint8_t* scale, int c, int ldq
   if ((c & 31) == 0) scale[c / 32] = fine ? e + 127 : 255;
 }
 
+// The 8-bit form of a row's u, whose elements are in v: zeros past the row's end.
+template <int NT, int VPT, bool AL>
+__device__ __forceinline__ void keep_row(const NormP& p, int64_t row, int tid, const float* v) {
+  const int ldq = (int)p.ldq;
+  uint8_t* q = p.q + row * ldq;
+  uint8_t* scale = p.scale + row * (ldq / 32);
+  if (AL) {
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) keep8(q, scale, (k * NT + tid) * 8, ldq, v + 8 * k);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8 * VPT; ++e) {  // a warp holds 32 neighbouring columns
+      const int c = column<NT, AL>(tid, e);
+      const uint32_t top = __reduce_max_sync(0xffffffffu, abs_bits(v[e]));
+      if (c >= ldq) continue;
+      const int x = act_exponent(top);
+      const bool fine = top < kInfBits;
+      q[c] = fine ? (uint8_t)e4m3x2(v[e] * act_unscale(x), 0.f) : 0;
+      if ((tid & 31) == 0) scale[c / 32] = fine ? x + 127 : 255;
+    }
+  }
+}
+
 template <typename T, int NT, int VPT, bool AL>
 __global__ void __launch_bounds__(cta_threads(NT)) k_norm(const NormP p) {
   constexpr int E = 8 * VPT;
@@ -232,38 +255,19 @@ __global__ void __launch_bounds__(cta_threads(NT)) k_norm(const NormP p) {
   }
   store_row<T, NT, VPT, AL>(static_cast<T*>(p.u) + row * p.ldu, tid, d, h);
   if (!p.q) return;
-  uint8_t* q = p.q + row * p.ldq;
-  uint8_t* scale = p.scale + row * (p.ldq / 32);
-  if (AL) {
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-      const int c = (k * NT + tid) * 8;
-      if (c >= d)  // the row's end inside its last block
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[8 * k + j] = 0.f;
-      keep8(q, scale, c, (int)p.ldq, h + 8 * k);
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int c = column<NT, AL>(tid, e);
-      const float v = c < d ? h[e] : 0.f;
-      const uint32_t top = __reduce_max_sync(0xffffffffu, abs_bits(v));
-      if (c >= p.ldq) continue;
-      const int x = act_exponent(top);
-      const bool fine = top < kInfBits;
-      q[c] = fine ? (uint8_t)e4m3x2(v * act_unscale(x), 0.f) : 0;
-      if ((tid & 31) == 0) scale[c / 32] = fine ? x + 127 : 255;
-    }
-  }
+  for (int e = 0; e < E; ++e)
+    if (column<NT, AL>(tid, e) >= d) h[e] = 0.f;
+  keep_row<NT, VPT, AL>(p, row, tid, h);
 }
 
 // ---- the ring: this thread's 8-element pieces of A arrays of a row, STAGES rows
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
+template <typename T, int NT, int VPT, int A, bool AL> struct Ring;
 template <typename T, int NT, int VPT, int A>
-struct Ring {
+struct Ring<T, NT, VPT, A, true> {
   static constexpr int kPiece = 8 * sizeof(T);
   static constexpr int kThreads = cta_threads(NT);
   static constexpr int kStage = A * VPT * kPiece * kThreads;
@@ -274,7 +278,9 @@ struct Ring {
   __device__ __forceinline__ uint32_t slot(int stage, int array, int k, int half) const {
     return base + stage * kStage + ((array * VPT + k) * (kPiece / 16) + half) * 16 * kThreads;
   }
-  __device__ __forceinline__ void fetch(int stage, int array, const T* row, int tid, int d) const {
+  __device__ __forceinline__ void fetch(int stage, int array, const void* p, int64_t ld, int64_t r,
+                                        int64_t, int tid, int d) const {
+    const T* row = static_cast<const T*>(p) + r * ld;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int c = (k * NT + tid) * 8;
@@ -283,6 +289,7 @@ struct Ring {
         for (int i = 0; i < kPiece / 16; ++i) copy16(slot(stage, array, k, i), row + c + i * (16 / sizeof(T)));
     }
   }
+  __device__ __forceinline__ void arrived() const {}
   __device__ __forceinline__ uint4 read16(uint32_t a) const {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -290,7 +297,8 @@ struct Ring {
     return v;
   }
   // piece k as 8 floats, zeros past the row's end
-  __device__ __forceinline__ void read(int stage, int array, int k, int tid, int d, float* v) const {
+  __device__ __forceinline__ void read(int stage, int array, const void*, int64_t, int64_t, int k, int tid,
+                                       int d, float* v) const {
     Raw8<T> raw = zero_raw<T>();
     if ((k * NT + tid) * 8 < d) {
       raw.a = read16(slot(stage, array, k, 0));
@@ -299,41 +307,102 @@ struct Ring {
     unpack(raw, v);
   }
 };
+// Rows that do not start on 16 bytes: the row's 16-byte aligned neighbourhood, as it lies in
+// memory, fetched by all of the row's threads and read back an element at a time (column
+// (8 k + j) NT + tid, so that a warp's accesses are consecutive).  Here threads do read each
+// other's slots: arrived() waits for all of them.  The elements around the row come along with
+// its first and last 16 bytes and are not used; where those 16 bytes stick out of the whole array
+// (its first and last row) the row's elements are copied one by one.
+template <typename T, int NT, int VPT, int A>
+struct Ring<T, NT, VPT, A, false> {
+  static constexpr int kRow = NT * VPT * 8 * (int)sizeof(T) + 16;
+  static constexpr int kStage = A * kRow * (cta_threads(NT) / NT);
+  uint32_t base;
+  __device__ __forceinline__ explicit Ring(void* smem) {
+    base = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) +
+           (NT == 32 ? (threadIdx.x >> 5) * A * kRow : 0);
+  }
+  __device__ __forceinline__ uint32_t row_slot(int stage, int array) const {
+    return base + stage * kStage + array * kRow;
+  }
+  __device__ __forceinline__ void fetch(int stage, int array, const void* p, int64_t ld, int64_t r,
+                                        int64_t tokens, int tid, int d) const {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p), hi = lo + ((tokens - 1) * ld + d) * sizeof(T);
+    const uintptr_t row = lo + r * ld * sizeof(T), from = row & ~(uintptr_t)15;
+    const int n = (int)((row - from + d * sizeof(T) + 15) / 16);
+    const uint32_t to = row_slot(stage, array);
+    for (int i = tid; i < n; i += NT) {
+      const uintptr_t at = from + 16 * i;
+      if (at >= lo && at + 16 <= hi) {
+        copy16(to + 16 * i, reinterpret_cast<const void*>(at));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16 / (int)sizeof(T); ++j) {
+          const uintptr_t e = at + j * sizeof(T);
+          if (e < lo || e >= hi) continue;
+          if constexpr (sizeof(T) == 2)
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + 16 * i + 2 * j),
+                         "h"(*reinterpret_cast<const uint16_t*>(e)) : "memory");
+          else
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + 16 * i + 4 * j),
+                         "r"(*reinterpret_cast<const uint32_t*>(e)) : "memory");
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void arrived() const {
+    if (NT == 32) __syncwarp();
+    else __syncthreads();
+  }
+  __device__ __forceinline__ void read(int stage, int array, const void* p, int64_t ld, int64_t r, int k,
+                                       int tid, int d, float* v) const {
+    const uint32_t at = row_slot(stage, array) +
+                        (uint32_t)((reinterpret_cast<uintptr_t>(p) + r * ld * sizeof(T)) & 15);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = (8 * k + j) * NT + tid;
+      v[j] = 0.f;
+      if (c >= d) continue;
+      if constexpr (sizeof(T) == 2) {
+        uint16_t w;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(w) : "r"(at + c * 2) : "memory");
+        v[j] = to_float(*reinterpret_cast<const T*>(&w));
+      } else {
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[j]) : "r"(at + c * 4) : "memory");
+      }
+    }
+  }
+};
 __device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void ring_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// u (and its 8-bit form) of one row from h, whose pieces are in v; the thread's pre-gains in w.
-template <typename T, int NT, int VPT>
-__device__ __forceinline__ void finish_row(const NormP& p, int64_t row, int tid, const float* v,
-                                           const float* w, float r) {
+// u (and its 8-bit form) of one row from h, whose elements are in v; the thread's pre-gains in w.
+template <typename T, int NT, int VPT, bool AL>
+__device__ __forceinline__ void finish_row(const NormP& p, int64_t row, int tid, float* v, const float* w,
+                                           float r) {
   const int d = p.features;
 #pragma unroll
-  for (int k = 0; k < VPT; ++k) {
-    const int c = (k * NT + tid) * 8;
-    float u[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) u[j] = c < d ? w[8 * k + j] * (v[8 * k + j] * r) : 0.f;
-    if (c < d) store8(static_cast<T*>(p.u) + row * p.ldu + c, u);
-    if (p.q) keep8(p.q + row * p.ldq, p.scale + row * (p.ldq / 32), c, (int)p.ldq, u);
-  }
+  for (int e = 0; e < 8 * VPT; ++e) v[e] = column<NT, AL>(tid, e) < d ? w[e] * (v[e] * r) : 0.f;
+  store_row<T, NT, VPT, AL>(static_cast<T*>(p.u) + row * p.ldu, tid, d, v);
+  if (p.q) keep_row<NT, VPT, AL>(p, row, tid, v);
 }
 
-template <typename T, int NT, int VPT, int STAGES>
+template <typename T, int NT, int VPT, bool AL, int STAGES>
 __global__ void __launch_bounds__(cta_threads(NT), ctas_per_sm(NT)) k_norm_stream(const NormP p) {
   constexpr int E = 8 * VPT, RPC = NT == 32 ? kWarpRows : 1;
   extern __shared__ uint4 ring_smem[];
   __shared__ float red[NT == 32 ? 1 : NT / 32];
-  const Ring<T, NT, VPT, 2> ring(ring_smem);
+  const Ring<T, NT, VPT, 2, AL> ring(ring_smem);
   const int tid = NT == 32 ? threadIdx.x & 31 : threadIdx.x;
   const int d = p.features;
   const int64_t step = (int64_t)gridDim.x * RPC;
   const int64_t first = (int64_t)blockIdx.x * RPC + (NT == 32 ? threadIdx.x >> 5 : 0);
   auto fetch = [&](int64_t row, int stage) {
     if (row < p.tokens) {
-      ring.fetch(stage, 0, static_cast<const T*>(p.x) + row * p.ldx, tid, d);
-      if (p.y) ring.fetch(stage, 1, static_cast<const T*>(p.y) + row * p.ldy, tid, d);
+      ring.fetch(stage, 0, p.x, p.ldx, row, p.tokens, tid, d);
+      if (p.y) ring.fetch(stage, 1, p.y, p.ldy, row, p.tokens, tid, d);
     }
     ring_commit();
   };
@@ -343,23 +412,24 @@ __global__ void __launch_bounds__(cta_threads(NT), ctas_per_sm(NT)) k_norm_strea
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
     float a[8], b[8];
-    gains<NT, true>(p.pre, tid, k, d, w + 8 * k);
-    gains<NT, true>(p.post, tid, k, d, a);
-    gains<NT, true>(p.gate, tid, k, d, b);
+    gains<NT, AL>(p.pre, tid, k, d, w + 8 * k);
+    gains<NT, AL>(p.post, tid, k, d, a);
+    gains<NT, AL>(p.gate, tid, k, d, b);
 #pragma unroll
     for (int j = 0; j < 8; ++j) c[8 * k + j] = a[j] * b[j];
   }
   int stage = 0;
   for (int64_t row = first; row < p.tokens; row += step) {
     ring_wait<STAGES - 2>();
+    ring.arrived();
     float h[E];
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) ring.read(stage, 0, k, tid, d, h + 8 * k);
+    for (int k = 0; k < VPT; ++k) ring.read(stage, 0, p.x, p.ldx, row, k, tid, d, h + 8 * k);
     float ss[1] = {0.f};
     if (p.y) {
       float y[E];
 #pragma unroll
-      for (int k = 0; k < VPT; ++k) ring.read(stage, 1, k, tid, d, y + 8 * k);
+      for (int k = 0; k < VPT; ++k) ring.read(stage, 1, p.y, p.ldy, row, k, tid, d, y + 8 * k);
       float f = p.s;
       if (p.post_norm) {
 #pragma unroll
@@ -370,7 +440,7 @@ __global__ void __launch_bounds__(cta_threads(NT), ctas_per_sm(NT)) k_norm_strea
       }
 #pragma unroll
       for (int e = 0; e < E; ++e) h[e] = fmaf(c[e], y[e] * f, h[e]);
-      if (p.h) store_row<T, NT, VPT, true>(static_cast<T*>(p.h) + row * p.ldh, tid, d, h);
+      if (p.h) store_row<T, NT, VPT, AL>(static_cast<T*>(p.h) + row * p.ldh, tid, d, h);
     }
     // the slots read in the last round take the next row
     fetch(row + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
@@ -378,9 +448,9 @@ __global__ void __launch_bounds__(cta_threads(NT), ctas_per_sm(NT)) k_norm_strea
     if (!p.u) continue;
 #pragma unroll
     for (int e = 0; e < E; ++e)
-      if (column<NT, true>(tid, e) < d) ss[0] = fmaf(h[e], h[e], ss[0]);
+      if (column<NT, AL>(tid, e) < d) ss[0] = fmaf(h[e], h[e], ss[0]);
     row_sum<NT, 1>(ss, red);
-    finish_row<T, NT, VPT>(p, row, tid, h, w, inv_sqrt(fmaf(ss[0], p.inv_d, p.eps)));
+    finish_row<T, NT, VPT, AL>(p, row, tid, h, w, inv_sqrt(fmaf(ss[0], p.inv_d, p.eps)));
   }
   ring_wait<0>();
 }
@@ -429,14 +499,14 @@ __device__ __forceinline__ void write_parts(const NormGradP& p, int tid, float* 
   }
 }
 
-template <typename T, int NT, int VPT, int STAGES>
+template <typename T, int NT, int VPT, bool AL, int STAGES>
 __global__ void __launch_bounds__(cta_threads(NT), ctas_per_sm(NT)) k_norm_grad_stream(const NormGradP p) {
   constexpr int E = 8 * VPT, RPC = NT == 32 ? kWarpRows : 1;
   extern __shared__ uint4 ring_smem[];
   __shared__ float red[NT == 32 ? 1 : 3 * NT / 32];
   grid_trigger();  // a grid of one round, whose CTAs fill the SMs
   enum { H, DU, DH, Y };
-  const Ring<T, NT, VPT, 4> ring(ring_smem);
+  const Ring<T, NT, VPT, 4, AL> ring(ring_smem);
   const int tid = NT == 32 ? threadIdx.x & 31 : threadIdx.x;
   const int d = p.features;
   const int64_t step = (int64_t)gridDim.x * RPC;
@@ -444,11 +514,11 @@ __global__ void __launch_bounds__(cta_threads(NT), ctas_per_sm(NT)) k_norm_grad_
   auto fetch = [&](int64_t row, int stage) {
     if (row < p.tokens) {
       if (p.du) {
-        ring.fetch(stage, H, static_cast<const T*>(p.h) + row * p.ldh, tid, d);
-        ring.fetch(stage, DU, static_cast<const T*>(p.du) + row * p.lddu, tid, d);
+        ring.fetch(stage, H, p.h, p.ldh, row, p.tokens, tid, d);
+        ring.fetch(stage, DU, p.du, p.lddu, row, p.tokens, tid, d);
       }
-      if (p.dh) ring.fetch(stage, DH, static_cast<const T*>(p.dh) + row * p.lddh, tid, d);
-      if (p.y) ring.fetch(stage, Y, static_cast<const T*>(p.y) + row * p.ldy, tid, d);
+      if (p.dh) ring.fetch(stage, DH, p.dh, p.lddh, row, p.tokens, tid, d);
+      if (p.y) ring.fetch(stage, Y, p.y, p.ldy, row, p.tokens, tid, d);
     }
     ring_commit();
   };
@@ -458,9 +528,9 @@ __global__ void __launch_bounds__(cta_threads(NT), ctas_per_sm(NT)) k_norm_grad_
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
     float a[8], b[8];
-    gains<NT, true>(p.pre, tid, k, d, w + 8 * k);
-    gains<NT, true>(p.post, tid, k, d, a);
-    gains<NT, true>(p.gate, tid, k, d, b);
+    gains<NT, AL>(p.pre, tid, k, d, w + 8 * k);
+    gains<NT, AL>(p.post, tid, k, d, a);
+    gains<NT, AL>(p.gate, tid, k, d, b);
 #pragma unroll
     for (int j = 0; j < 8; ++j) c[8 * k + j] = p.s * a[j] * b[j];
   }
@@ -469,6 +539,7 @@ __global__ void __launch_bounds__(cta_threads(NT), ctas_per_sm(NT)) k_norm_grad_
   int stage = 0;
   for (int64_t row = first; row < p.tokens; row += step) {
     ring_wait<STAGES - 2>();
+    ring.arrived();
     // the slots read in the last round take the next row
     fetch(row + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
     float sum[3] = {0.f, 0.f, 0.f};
@@ -476,8 +547,8 @@ __global__ void __launch_bounds__(cta_threads(NT), ctas_per_sm(NT)) k_norm_grad_
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
         float h[8], u[8];
-        ring.read(stage, H, k, tid, d, h);
-        ring.read(stage, DU, k, tid, d, u);
+        ring.read(stage, H, p.h, p.ldh, row, k, tid, d, h);
+        ring.read(stage, DU, p.du, p.lddu, row, k, tid, d, u);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           sum[0] = fmaf(h[j], h[j], sum[0]);
@@ -488,7 +559,7 @@ __global__ void __launch_bounds__(cta_threads(NT), ctas_per_sm(NT)) k_norm_grad_
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
         float y[8];
-        ring.read(stage, Y, k, tid, d, y);
+        ring.read(stage, Y, p.y, p.ldy, row, k, tid, d, y);
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum[2] = fmaf(y[j], y[j], sum[2]);
       }
@@ -500,14 +571,14 @@ __global__ void __launch_bounds__(cta_threads(NT), ctas_per_sm(NT)) k_norm_grad_
     for (int k = 0; k < VPT; ++k) {
       float h[8], u[8];
       if (p.dh) {
-        ring.read(stage, DH, k, tid, d, g + 8 * k);
+        ring.read(stage, DH, p.dh, p.lddh, row, k, tid, d, g + 8 * k);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) g[8 * k + j] = 0.f;
       }
       if (p.du) {
-        ring.read(stage, H, k, tid, d, h);
-        ring.read(stage, DU, k, tid, d, u);
+        ring.read(stage, H, p.h, p.ldh, row, k, tid, d, h);
+        ring.read(stage, DU, p.du, p.lddu, row, k, tid, d, u);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int e = 8 * k + j;
@@ -517,14 +588,14 @@ __global__ void __launch_bounds__(cta_threads(NT), ctas_per_sm(NT)) k_norm_grad_
         }
       }
     }
-    if (p.dx) store_row<T, NT, VPT, true>(static_cast<T*>(p.dx) + row * p.lddx, tid, d, g);
+    if (p.dx) store_row<T, NT, VPT, AL>(static_cast<T*>(p.dx) + row * p.lddx, tid, d, g);
     if (p.y) {
       const float ry = p.post_norm ? inv_sqrt(fmaf(sum[2], p.inv_d, p.eps)) : 1.f;
       float dot[1] = {0.f};
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
         float y[8];
-        ring.read(stage, Y, k, tid, d, y);
+        ring.read(stage, Y, p.y, p.ldy, row, k, tid, d, y);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int e = 8 * k + j;
@@ -540,17 +611,17 @@ __global__ void __launch_bounds__(cta_threads(NT), ctas_per_sm(NT)) k_norm_grad_
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
           float y[8];
-          ring.read(stage, Y, k, tid, d, y);
+          ring.read(stage, Y, p.y, p.ldy, row, k, tid, d, y);
 #pragma unroll
           for (int j = 0; j < 8; ++j) g[8 * k + j] = ry * fmaf(-y[j] * ry, m2, g[8 * k + j]);
         }
       }
-      if (p.dy) store_row<T, NT, VPT, true>(static_cast<T*>(p.dy) + row * p.lddy, tid, d, g);
+      if (p.dy) store_row<T, NT, VPT, AL>(static_cast<T*>(p.dy) + row * p.lddy, tid, d, g);
     }
     if (++stage == STAGES) stage = 0;
   }
   ring_wait<0>();
-  write_parts<NT, VPT, true>(p, tid, apre, apost);
+  write_parts<NT, VPT, AL>(p, tid, apre, apost);
 }
 
 // The form without a ring.  Rows of more than two pieces a thread keep the column sums in
@@ -743,13 +814,22 @@ cudaError_t allow_smem(const void* kernel, int bytes) {
 }
 
 // Rows of the rings: three, two where three do not fit, none (the direct form) past that.
-// fp32 forward takes the direct form: a thread's piece is two 16-byte copies there, half a
-// sector each, and the stream of 8192 x 4096 ran at 133 us against 100 us.
-template <typename T, int NT, int VPT, int A>
+template <typename T, int NT, int VPT, int A, bool AL>
 int ring_stages() {
-  if (sizeof(T) == 4 && A == 2) return 0;
-  constexpr int stage = Ring<T, NT, VPT, A>::kStage * ctas_per_sm(NT);
+  constexpr int stage = Ring<T, NT, VPT, A, AL>::kStage * ctas_per_sm(NT);
   return VPT > 2 ? 0 : 3 * stage <= kSmemMost ? 3 : 2 * stage <= kSmemMost ? 2 : 0;
+}
+
+// Launches the streaming kernel of A arrays, if its ring fits; false if it does not.
+template <typename T, int NT, int VPT, int A, bool AL, typename P>
+bool launch_stream(const P& p, unsigned grid, cudaStream_t s, cudaError_t* e, void (*three)(P), void (*two)(P)) {
+  const int stages = ring_stages<T, NT, VPT, A, AL>();
+  if (stages == 0) return false;
+  const int bytes = stages * Ring<T, NT, VPT, A, AL>::kStage;
+  auto* kernel = stages == 3 ? three : two;
+  *e = allow_smem((const void*)kernel, bytes);
+  if (*e == cudaSuccess) kernel<<<grid, cta_threads(NT), bytes, s>>>(p);
+  return true;
 }
 
 template <typename T>
@@ -758,15 +838,15 @@ cudaError_t launch_norm(const NormP& p, bool al, cudaStream_t s) {
   by_width(p.features, [&](auto nt, auto vpt) {
     constexpr int NT = decltype(nt)::value, VPT = decltype(vpt)::value;
     const int64_t rows = row_ctas(p.tokens, NT), fixed = stream_ctas(NT);
-    if constexpr (VPT <= 2) {
-      const int stages = ring_stages<T, NT, VPT, 2>();
-      if (al && stages > 0) {
-        const int bytes = stages * Ring<T, NT, VPT, 2>::kStage;
-        auto* kernel = stages == 3 ? k_norm_stream<T, NT, VPT, 3> : k_norm_stream<T, NT, VPT, 2>;
-        e = allow_smem((const void*)kernel, bytes);
-        if (e == cudaSuccess) kernel<<<(unsigned)std::min(rows, fixed), cta_threads(NT), bytes, s>>>(p);
+    // fp32 forward takes the direct form: a thread's piece is two 16-byte copies there, half a
+    // sector each, and the stream of 8192 x 4096 ran at 133 us against 85 us
+    if constexpr (VPT <= 2 && sizeof(T) == 2) {
+      const unsigned grid = (unsigned)std::min(rows, fixed);
+      if (al ? launch_stream<T, NT, VPT, 2, true>(p, grid, s, &e, k_norm_stream<T, NT, VPT, true, 3>,
+                                                  k_norm_stream<T, NT, VPT, true, 2>)
+             : launch_stream<T, NT, VPT, 2, false>(p, grid, s, &e, k_norm_stream<T, NT, VPT, false, 3>,
+                                                   k_norm_stream<T, NT, VPT, false, 2>))
         return;
-      }
     }
     if (al) k_norm<T, NT, VPT, true><<<(unsigned)rows, cta_threads(NT), 0, s>>>(p);
     else k_norm<T, NT, VPT, false><<<(unsigned)rows, cta_threads(NT), 0, s>>>(p);
@@ -780,14 +860,11 @@ cudaError_t launch_grad(const NormGradP& p, bool al, unsigned grid, cudaStream_t
   by_width(p.features, [&](auto nt, auto vpt) {
     constexpr int NT = decltype(nt)::value, VPT = decltype(vpt)::value;
     if constexpr (VPT <= 2) {
-      const int stages = ring_stages<T, NT, VPT, 4>();
-      if (al && stages > 0) {
-        const int bytes = stages * Ring<T, NT, VPT, 4>::kStage;
-        auto* kernel = stages == 3 ? k_norm_grad_stream<T, NT, VPT, 3> : k_norm_grad_stream<T, NT, VPT, 2>;
-        e = allow_smem((const void*)kernel, bytes);
-        if (e == cudaSuccess) kernel<<<grid, cta_threads(NT), bytes, s>>>(p);
+      if (al ? launch_stream<T, NT, VPT, 4, true>(p, grid, s, &e, k_norm_grad_stream<T, NT, VPT, true, 3>,
+                                                  k_norm_grad_stream<T, NT, VPT, true, 2>)
+             : launch_stream<T, NT, VPT, 4, false>(p, grid, s, &e, k_norm_grad_stream<T, NT, VPT, false, 3>,
+                                                   k_norm_grad_stream<T, NT, VPT, false, 2>))
         return;
-      }
     }
     const int bytes = VPT > 2 ? 2 * 8 * VPT * NT * 4 : 0;
     auto* kernel = al ? k_norm_grad<T, NT, VPT, true> : k_norm_grad<T, NT, VPT, false>;

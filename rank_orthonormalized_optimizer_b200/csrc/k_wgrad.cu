@@ -218,8 +218,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   uint8_t* sA = smem;
   uint8_t* sB = sA + SA * A_BYTES;
   uint8_t* sQ = sB + SB * B_BYTES;
-  uint32_t* sS = reinterpret_cast<uint32_t*>(sQ + SQ * Q_BYTES);  // [stage][token]: 4 scale bytes
-  uint64_t* q_full = reinterpret_cast<uint64_t*>(sS + SQ * BK);   // the 8-bit tile and its scales
+  uint32_t* sS = reinterpret_cast<uint32_t*>(sQ + SQ * Q_BYTES);  // [stage][2][token]: scale bytes
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(sS + SQ * 2 * BK);   // the 8-bit tile and its scales
   uint64_t* q_empty = q_full + SQ;
   uint64_t* b_full = q_empty + SQ;
   uint64_t* b_empty = b_full + SB;
@@ -339,7 +339,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
           : "memory");
       wait_drain(drain, 0);
     } else if (warp == 3) {
-      // ---------------- scale bytes: four per token, two tokens a lane
+      // ---------------- scale bytes: the word of a token's four, or the two words that they
+      // lie in, two tokens a lane
+      const uintptr_t begin = reinterpret_cast<uintptr_t>(p.scale), end = begin + p.tokens * p.ld_scale;
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -353,26 +355,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int64_t tok = (int64_t)kb * BK + lane + 32 * i;
-            const bool in = tok < p.tokens;
-            const uint8_t* s = p.scale + (in ? tok * p.ld_scale + c : 0);
-            uint32_t* to = sS + stage * BK + lane + 32 * i;
-            if (p.scale4) {  // asynchronous: the ring's stages are all in flight
-              asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(to)),
-                           "l"(valid == 4 ? s : p.scale), "r"(in && valid == 4 ? 4 : 0)
-                           : "memory");
-            } else {
-              uint32_t w = 0;
+            const uintptr_t at = begin + (tok < p.tokens && valid > 0 ? tok * p.ld_scale + c : 0);
+            const int bytes = tok < p.tokens ? valid : 0;
 #pragma unroll
-              for (int b = 0; b < 4; ++b)
-                if (in && b < valid) w |= (uint32_t)__ldg(s + b) << (8 * b);
-              *to = w;
+            for (int h = 0; h < 2; ++h) {
+              if (h == 1 && p.scale4) break;
+              const uintptr_t word = (at & ~(uintptr_t)3) + 4 * h;
+              const uint32_t to = smem_u32(sS + (stage * 2 + h) * BK + lane + 32 * i);
+              if (bytes == 0 || word >= at + bytes) {
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(0u) : "memory");
+              } else if (word >= begin && word + 4 <= end) {  // asynchronous: the whole ring in flight
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(word) : "memory");
+              } else {  // a word that sticks out of the array, at its first or last token
+                uint32_t w = 0;
+                for (int b = 0; b < 4; ++b)
+                  if (word + b >= begin && word + b < end)
+                    w |= (uint32_t)*reinterpret_cast<const uint8_t*>(word + b) << (8 * b);
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(w) : "memory");
+              }
             }
           }
-          if (p.scale4)
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(q_full + stage))
-                         : "memory");
-          else
-            mbar_arrive(q_full + stage);
+          __threadfence_block();
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(q_full + stage))
+                       : "memory");
           if (++stage == SQ) { stage = 0; phase ^= 1; }
         }
       }
@@ -392,25 +397,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
     const uint32_t dst0 = (c >> 2) * 8192 + k0 * 128 + ((2 * (c & 3) ^ r7) << 4);
     const uint32_t base = smem_u32(smem);
     const uint32_t byte = 0x4440 | c >> 1;      // this thread's scale byte of a token's word
+    const uint32_t skew = (uint32_t)reinterpret_cast<uintptr_t>(p.scale);
     int sq = group % SQ, sa = group % SA, sb = group % SB;
     uint32_t pq = 0, pa = 0, pb = 0;
     int skip = group;                           // stages until this group's next
     bool ok = true;
     for (int u = pair; u < units && ok; u += pairs) {
       const Unit t = unit_of<BN>(p, u);
-      int kb = t.kb0 + skip;
+      int kb = t.kb0 + skip;  // (a tile's first scale byte is a multiple of 4 from its row's)
       for (; kb < t.kb1; kb += kGroups) {
         const bool w = wait_bounded(q_full + sq, pq, p.max_spins, abort) &&
                        wait_bounded(a_empty + sa, pa ^ 1, p.max_spins, abort);
         if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
         const uint32_t src = base + (SA * A_BYTES + SB * B_BYTES) + sq * Q_BYTES + src0;
-        const uint32_t scale = base + (SA * A_BYTES + SB * B_BYTES + SQ * Q_BYTES) + (sq * BK + k0) * 4;
+        const uint32_t scale = base + (SA * A_BYTES + SB * B_BYTES + SQ * Q_BYTES) + (sq * 2 * BK + k0) * 4;
         const uint32_t dst = base + sa * A_BYTES + dst0;
         uint32_t E[kItems], top = 0;
         uint4 next = lds128(src);
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
-          E[i] = __byte_perm(lds32(scale + 64 * i), 0, byte);
+          if (p.scale4) {
+            E[i] = __byte_perm(lds32(scale + 64 * i), 0, byte);
+          } else {  // the byte after the token's place in its first word
+            const uint32_t off = skew + (uint32_t)(kb * BK + k0 + 16 * i) * (uint32_t)p.ld_scale & 3;
+            E[i] = __byte_perm(lds32(scale + 64 * i), lds32(scale + 4 * BK + 64 * i), off + (c >> 1)) & 255u;
+          }
           top = max(top, E[i]);
         }
         // up to E = 134 the factor 2^(E - 127) 2^120 is one bf16 number; above, two products
@@ -565,14 +576,20 @@ __global__ void __launch_bounds__(1024) k_wgrad_join(const WgradP p, int bn) {
   *g = block[tx][ty] + (p.accumulate ? *g : 0.f);
 }
 
-// D into rows that a TMA map can take (a multiple of 8 columns, the rest zero).
+// D into rows that a TMA map can take (a multiple of 8 columns, the rest zero), 8 columns a thread.
+template <typename I>
 __global__ void __launch_bounds__(256) k_wgrad_pad(const __nv_bfloat16* d, int64_t ldd,
                                                    __nv_bfloat16* out, int64_t ldo, int64_t tokens,
-                                                   int64_t n) {
-  const int64_t total = tokens * ldo;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t row = i / ldo, col = i - row * ldo;
-    out[i] = col < n ? d[row * ldd + col] : __float2bfloat16_rn(0.f);
+                                                   int64_t n, const RowDiv<I> row_of) {
+  const I per_row = (I)(ldo / 8), total = (I)(tokens * per_row);
+  const unsigned short* from = reinterpret_cast<const unsigned short*>(d);
+  for (I i = (I)blockIdx.x * 256 + threadIdx.x; i < total; i += (I)gridDim.x * 256) {
+    const I r = row_of(i);
+    const int64_t row = r, col = (int64_t)(i - r * per_row) * 8;
+    uint32_t v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = col + j < n ? __ldg(from + row * ldd + col + j) : 0u;
+    st_vec(out + row * ldo + col, make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16));
   }
 }
 
@@ -687,7 +704,7 @@ dion_status check_source(const dion_grad_source& s, int i) {
 
 template <int BN>
 dion_status launch(const CUtensorMap& mq, const CUtensorMap& md, const WgradP& p, int sms, cudaStream_t s) {
-  constexpr size_t smem = 1024 + SA * A_BYTES + SB * BK * BN + SQ * (Q_BYTES + BK * 4) +
+  constexpr size_t smem = 1024 + SA * A_BYTES + SB * BK * BN + SQ * (Q_BYTES + 2 * BK * 4) +
                           (2 * SQ + 2 * SB + 2 * SA + 5) * 8 + 16;
   const cudaError_t e = cudaFuncSetAttribute(k_wgrad<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)smem);
@@ -711,8 +728,11 @@ dion_status one_grad(const dion_grad_source& src, int accumulate, char* ws, int3
   int64_t ldd = src.ldd;
   if (g.pad) {
     __nv_bfloat16* copy = reinterpret_cast<__nv_bfloat16*>(ws + g.parts_bytes);
-    k_wgrad_pad<<<sms * 8, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(src.d), src.ldd, copy, g.ldd,
-                                        tokens, n);
+    const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(src.d);
+    if (tokens * (g.ldd / 8) + sms * 8 * 256 < (int64_t(1) << 31))
+      k_wgrad_pad<uint32_t><<<sms * 8, 256, 0, s>>>(from, src.ldd, copy, g.ldd, tokens, n, RowDiv<uint32_t>(g.ldd / 8));
+    else
+      k_wgrad_pad<int64_t><<<sms * 8, 256, 0, s>>>(from, src.ldd, copy, g.ldd, tokens, n, RowDiv<int64_t>(g.ldd / 8));
     DION_TRY(launch_status("k_wgrad_pad"));
     d = copy;
     ldd = g.ldd;

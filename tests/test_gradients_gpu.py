@@ -68,7 +68,9 @@ NORM_SHAPES = [(1, 1, 0, 0), (3, 7, 0, 0), (5, 64, 0, 0), (4, 256, 0, 0), (9, 26
                (2, 12345, 0, 0), (4, 512, 0, 1), (3, 4096, 3, 5), (1300, 96, 0, 0),
                # batches that are streamed, ragged in rows and columns
                (4801, 104, 0, 0), (5000, 264, 8, 0), (2500, 1016, 0, 0), (1201, 2048, 0, 0),
-               (607, 4088, 8, 0), (301, 8192, 0, 0), (301, 8200, 0, 0)]
+               (607, 4088, 8, 0), (301, 8192, 0, 0), (301, 8200, 0, 0),
+               (607, 4095, 0, 0), (1203, 2041, 3, 5), (2500, 1015, 0, 1), (5000, 261, 0, 0),
+               (4801, 99, 2, 3), (301, 8191, 1, 7)]
 
 
 def _norm_inputs(t, d, pad, shift, dtype, seed):
@@ -298,7 +300,7 @@ def test_act_special_blocks():
 # (tokens, m, n): one token, ragged tokens, tiles' borders, odd n (copied rows), many splits
 WGRAD_SHAPES = [(1, 8, 8), (1, 1, 1), (3, 40, 24), (63, 128, 64), (64, 128, 256), (65, 129, 65),
                 (255, 256, 128), (256, 32, 512), (257, 96, 264), (1000, 200, 72), (700, 130, 300),
-                (4099, 256, 128), (515, 1000, 777), (5000, 64, 8), (2048, 640, 1408), (300, 3, 1001)]
+                (4099, 256, 128), (515, 1000, 777), (5000, 64, 8), (2048, 640, 1408), (300, 3, 1001), (517, 2000, 96), (700, 333, 257)]
 
 
 def _wgrad_inputs(t, m, n, seed, pad=0, shift=0):
