@@ -5,7 +5,8 @@
 // HBM with no reuse, 3.03 bytes per bf16 element; what bounds them is the copy bandwidth.
 // A thread moves 32 bytes of a row (16 elements of the 2-byte types, so two neighbouring lanes
 // share a block and its maximum takes a shuffle), 16 where the rows only start on 16 bytes,
-// kUnroll pieces in flight; other rows go one element a lane, a warp to a block.
+// kUnroll pieces in flight.  Rows without alignment are read 8 single elements a thread (their
+// 8-bit rows are aligned all the same) and written one element a lane, a warp to a block.
 #include "operator.h"
 #include "rows.cuh"
 
@@ -16,7 +17,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;
-constexpr int kBlocks = 8;  // blocks of a warp in flight, in the form without vectors
+constexpr int kBlocks = 8;  // blocks of a warp in flight, in the load without vectors
 
 struct ActP {
   const void* x;   // save: source; load: destination (cast)
@@ -26,16 +27,31 @@ struct ActP {
   int64_t tokens, features, ld;  // ld = features rounded up to 32
 };
 
-// 8 H elements at 16 H bytes (2-byte types) or, H = 1, 32 bytes (fp32).
+// 8 H elements of a row at once, or one by one (H = 0: rows without alignment; their lines stay
+// in L1 between the accesses), n of them inside the row.
 template <typename T, int H>
-__device__ __forceinline__ void load_pieces(const T* p, Raw8<T>* raw) {
-  if constexpr (H == 2) ld_stream32(p, raw[0].a, raw[1].a);
-  else raw[0] = load_raw(p);
+__device__ __forceinline__ void load_pieces(const T* p, int n, Raw8<T>* raw) {
+  if constexpr (H == 2) {
+    ld_stream32(p, raw[0].a, raw[1].a);
+  } else if constexpr (H == 1) {
+    raw[0] = load_raw(p);
+  } else if constexpr (sizeof(T) == 2) {
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = j < n ? __ldg(reinterpret_cast<const unsigned short*>(p) + j) : 0u;
+    raw[0].a = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+  } else {
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = j < n ? __ldg(reinterpret_cast<const uint32_t*>(p) + j) : 0u;
+    raw[0].a = make_uint4(w[0], w[1], w[2], w[3]);
+    raw[0].b = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
 
-template <typename T, typename I, int H>
+template <typename T, typename I, int VEC>
 __global__ void __launch_bounds__(kThreads) k_act_save(const ActP p, const RowDiv<I> row_of) {
-  constexpr int N = 8 * H;
+  constexpr int H = VEC == 2 ? 2 : 1, N = 8 * H;
   const I per_row = (I)(p.ld / N), total = (I)(p.tokens * per_row);
   const T* x = static_cast<const T*>(p.x);
   const I stride = (I)gridDim.x * kThreads;
@@ -50,7 +66,7 @@ __global__ void __launch_bounds__(kThreads) k_act_save(const ActP p, const RowDi
       const I i = i0 + u * stride, r = row_of(i);
       row[u] = r;
       col[u] = (int)(i - r * per_row) * N;
-      if (i < total && col[u] < p.features) load_pieces<T, H>(x + row[u] * p.ldx + col[u], raw[u]);
+      if (i < total && col[u] < p.features) load_pieces<T, VEC>(x + row[u] * p.ldx + col[u], (int)min((int64_t)8, p.features - col[u]), raw[u]);
       else
 #pragma unroll
         for (int h = 0; h < H; ++h) raw[u][h] = zero_raw<T>();
@@ -79,33 +95,6 @@ __global__ void __launch_bounds__(kThreads) k_act_save(const ActP p, const RowDi
         else *reinterpret_cast<uint2*>(q) = make_uint2(o[0], o[1]);
         if (i % (4 / H) == 0) p.scale[row[u] * (p.ld / 32) + col[u] / 32] = fine ? e + 127 : 255;
       }
-    }
-  }
-}
-
-template <typename T, typename I>
-__global__ void __launch_bounds__(kThreads) k_act_save_any(const ActP p, const RowDiv<I> row_of) {
-  const I per_row = (I)(p.ld / 32), total = (I)(p.tokens * per_row);
-  const T* x = static_cast<const T*>(p.x);
-  const int lane = threadIdx.x & 31;
-  const I stride = (I)gridDim.x * (kThreads / 32);
-  for (I b0 = (I)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; b0 < total; b0 += stride * kBlocks) {
-    float v[kBlocks];
-#pragma unroll
-    for (int u = 0; u < kBlocks; ++u) {
-      const I b = b0 + u * stride, r = row_of(b);
-      const int64_t col = (int64_t)(b - r * per_row) * 32 + lane;
-      v[u] = b < total && col < p.features ? to_float(x[(int64_t)r * p.ldx + col]) : 0.f;
-    }
-#pragma unroll
-    for (int u = 0; u < kBlocks; ++u) {
-      const I b = b0 + u * stride;
-      if (b >= total) break;
-      const uint32_t top = __reduce_max_sync(0xffffffffu, abs_bits(v[u]));
-      const int e = act_exponent(top);
-      const bool fine = top < kInfBits;
-      p.q[(int64_t)b * 32 + lane] = fine ? (uint8_t)e4m3x2(v[u] * act_unscale(e), 0.f) : 0;
-      if (lane == 0) p.scale[b] = fine ? e + 127 : 255;
     }
   }
 }
@@ -183,22 +172,18 @@ __global__ void __launch_bounds__(kThreads) k_act_load_any(const ActP p, const R
 
 template <typename T, typename I, int H>
 void launch_as(const ActP& p, bool save, unsigned grid, cudaStream_t s) {
-  const RowDiv<I> row_of(H > 0 ? p.ld / (8 * H) : p.ld / 32);
-  if constexpr (H > 0) {
-    if (save) k_act_save<T, I, H><<<grid, kThreads, 0, s>>>(p, row_of);
-    else k_act_load<T, I, H><<<grid, kThreads, 0, s>>>(p, row_of);
-  } else {
-    if (save) k_act_save_any<T, I><<<grid, kThreads, 0, s>>>(p, row_of);
-    else k_act_load_any<T, I><<<grid, kThreads, 0, s>>>(p, row_of);
-  }
+  if (save) k_act_save<T, I, H><<<grid, kThreads, 0, s>>>(p, RowDiv<I>(p.ld / (H == 2 ? 16 : 8)));
+  else if constexpr (H > 0) k_act_load<T, I, H><<<grid, kThreads, 0, s>>>(p, RowDiv<I>(p.ld / (8 * H)));
+  else k_act_load_any<T, I><<<grid, kThreads, 0, s>>>(p, RowDiv<I>(p.ld / 32));
 }
 
-// H pieces of 8 elements to a thread; 0: the form without vectors.
+// H pieces of 8 elements to a thread; 0: the forms for rows without alignment.
 template <typename T, int H>
 void launch(const ActP& p, bool save, int sms, cudaStream_t s) {
-  const int64_t items = p.tokens * (H > 0 ? p.ld / (8 * H) : p.ld / 32);  // a thread's, or a warp's
+  const bool by_warp = !save && H == 0;
+  const int64_t items = p.tokens * (by_warp ? p.ld / 32 : p.ld / (H == 2 ? 16 : 8));
   const int64_t cap = (int64_t)sms * 8;
-  const int64_t per_cta = H > 0 ? kThreads * kUnroll : kThreads / 32;
+  const int64_t per_cta = by_warp ? kThreads / 32 : kThreads * kUnroll;
   const unsigned grid = (unsigned)std::min((items + per_cta - 1) / per_cta, cap);
   // indexes in 32 bits where all of them fit (a loop's last step overshoots by its stride):
   // the division by the row length is what costs

@@ -47,10 +47,10 @@ __device__ __forceinline__ int64_t load_id(const void* ids, int id64, int64_t t)
 }
 
 // One item: VEC consecutive elements of an output row.
-constexpr int kLookups = 4;  // items of a thread in flight
+constexpr int kLookups = 4;  // items of a thread in flight (of single elements twice as many)
 template <typename TI, typename TO, int VEC, typename I>
 __global__ void __launch_bounds__(kThreads) k_embed_lookup(const LookupP p, const RowDiv<I> row_of) {
-  constexpr int U = kLookups;
+  constexpr int U = VEC == 1 ? 2 * kLookups : kLookups;
   const I per_row = (I)(p.features / VEC), total = (I)(p.tokens * per_row);
   const I stride = (I)gridDim.x * kThreads;
   const TI* table = static_cast<const TI*>(p.table);
@@ -98,7 +98,7 @@ void launch_lookup(const LookupP& p, bool vec, int sms, cudaStream_t s) {
   const int64_t want = (items + kThreads - 1) / kThreads, cap = (int64_t)sms * 8;
   const unsigned grid = (unsigned)(want < cap ? want : cap);
   // as the 8-bit form's: 32-bit indexes where they fit
-  const bool small = items + cap * kThreads * kLookups < (int64_t(1) << 31);
+  const bool small = items + cap * kThreads * 2 * kLookups < (int64_t(1) << 31);
   const int64_t per_row = vec ? p.features / 8 : p.features;
   if (small) {
     auto* kernel = vec ? k_embed_lookup<TI, TO, 8, uint32_t> : k_embed_lookup<TI, TO, 1, uint32_t>;

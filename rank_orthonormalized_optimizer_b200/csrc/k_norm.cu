@@ -840,12 +840,13 @@ cudaError_t launch_norm(const NormP& p, bool al, cudaStream_t s) {
     const int64_t rows = row_ctas(p.tokens, NT), fixed = stream_ctas(NT);
     // fp32 forward takes the direct form: a thread's piece is two 16-byte copies there, half a
     // sector each, and the stream of 8192 x 4096 ran at 133 us against 85 us
-    if constexpr (VPT <= 2 && sizeof(T) == 2) {
+    if constexpr (VPT <= 2) {
       const unsigned grid = (unsigned)std::min(rows, fixed);
-      if (al ? launch_stream<T, NT, VPT, 2, true>(p, grid, s, &e, k_norm_stream<T, NT, VPT, true, 3>,
+      if ((sizeof(T) == 2 || !al) &&
+          (al ? launch_stream<T, NT, VPT, 2, true>(p, grid, s, &e, k_norm_stream<T, NT, VPT, true, 3>,
                                                   k_norm_stream<T, NT, VPT, true, 2>)
              : launch_stream<T, NT, VPT, 2, false>(p, grid, s, &e, k_norm_stream<T, NT, VPT, false, 3>,
-                                                   k_norm_stream<T, NT, VPT, false, 2>))
+                                                   k_norm_stream<T, NT, VPT, false, 2>)))
         return;
     }
     if (al) k_norm<T, NT, VPT, true><<<(unsigned)rows, cta_threads(NT), 0, s>>>(p);
