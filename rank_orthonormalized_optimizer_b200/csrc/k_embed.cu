@@ -439,6 +439,63 @@ __device__ __forceinline__ void write_zeros(const GradP& p, int64_t first) {
   }
 }
 
+// Rows that do not start on 16 bytes: their 16-byte aligned neighbourhoods as they lie in memory,
+// kGroup rows at a time into one of two buffers (cp.async), read back element by element.  The
+// elements around a row come along and are not used; 16 bytes that stick out of the whole array
+// (its first and last row) are copied one element at a time.
+template <typename T, int NT>
+struct RowStage {
+  static constexpr int kRow = NT * 8 * (int)sizeof(T) + 16;
+  static constexpr int kGroup = sizeof(T) == 4 ? 4 : 8;
+  static constexpr int kBytes = 2 * kGroup * kRow;
+  uint32_t base;
+  uintptr_t lo, hi;  // the array
+  __device__ __forceinline__ RowStage(void* smem, const GradP& p) {
+    base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+    lo = reinterpret_cast<uintptr_t>(p.dout);
+    hi = lo + ((p.tokens - 1) * p.ldo + p.features) * sizeof(T);
+  }
+  __device__ __forceinline__ uintptr_t address(const GradP& p, uint32_t pos, int64_t col0) const {
+    return lo + (pos * p.ldo + col0) * sizeof(T);
+  }
+  // the columns [col0, col0 + cols) of positions val[0 .. rows)
+  __device__ __forceinline__ void fetch(const GradP& p, int buffer, const uint32_t* val, int rows,
+                                        int64_t col0, int cols) const {
+    constexpr int kPieces = kRow / 16;
+    for (int i = threadIdx.x; i < rows * kPieces; i += NT) {
+      const int r = i / kPieces, piece = i % kPieces;
+      const uintptr_t row = address(p, val[r], col0), at = (row & ~(uintptr_t)15) + 16 * piece;
+      if (at >= row + cols * sizeof(T)) continue;
+      const uint32_t to = base + (buffer * kGroup + r) * kRow + 16 * piece;
+      if (at >= lo && at + 16 <= hi) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(at) : "memory");
+      } else {
+        for (int j = 0; j < 16 / (int)sizeof(T); ++j) {
+          const uintptr_t e = at + j * sizeof(T);
+          if (e < lo || e >= hi) continue;
+          if constexpr (sizeof(T) == 2)
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + 2 * j), "h"(*reinterpret_cast<const uint16_t*>(e)) : "memory");
+          else
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + 4 * j), "r"(*reinterpret_cast<const uint32_t*>(e)) : "memory");
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  __device__ __forceinline__ float read(const GradP& p, int buffer, int r, uint32_t pos, int64_t col0, int c) const {
+    const uint32_t at = base + (buffer * kGroup + r) * kRow + (uint32_t)(address(p, pos, col0) & 15) + c * (int)sizeof(T);
+    if constexpr (sizeof(T) == 2) {
+      uint16_t w;
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(w) : "r"(at) : "memory");
+      return to_float(*reinterpret_cast<const T*>(&w));
+    } else {
+      float v;
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+      return v;
+    }
+  }
+};
+
 template <typename T, int NT, bool AL>
 __global__ void __launch_bounds__(NT) k_embed_sum(const GradP p) {
   grid_wait();
@@ -447,74 +504,86 @@ __global__ void __launch_bounds__(NT) k_embed_sum(const GradP p) {
     return;
   }
   __shared__ uint32_t key[kSeg + 2], val[kSeg];  // key[0], key[n + 1]: the neighbours
+  __shared__ int met;                            // positions before the padding, which is sorted last
+  extern __shared__ uint4 stage_smem[];
   const int64_t seg = blockIdx.x / p.col_ctas;
   const int64_t col0 = (blockIdx.x - seg * p.col_ctas) * (8 * NT);
   const int64_t s0 = seg * kSeg;
-  const int n = (int)min((int64_t)kSeg, p.tokens - s0);
-  const uint32_t none = 0xffffffffu;
-  for (int i = threadIdx.x; i < n + 2; i += NT) {
+  const int in = (int)min((int64_t)kSeg, p.tokens - s0);
+  if (threadIdx.x == 0) met = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < in + 2; i += NT) {
     const int64_t at = s0 + i - 1;
-    key[i] = at >= 0 && at < p.tokens ? p.key[at] : none;
-    if (i >= 1 && i <= n) val[i - 1] = p.val[at];
+    key[i] = at >= 0 && at < p.tokens ? p.key[at] : 0xffffffffu;
+    if (i >= 1 && i <= in) {
+      val[i - 1] = p.val[at];
+      if (key[i] < p.vocab) atomicAdd(&met, 1);
+    }
   }
   __syncthreads();
-  constexpr int U = AL ? 8 : 4;  // rows in flight
+  const int n = met;
   float acc[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) acc[e] = 0.f;
   bool began = key[0] == key[1];  // the current run began in an earlier segment
-  const T* dout = static_cast<const T*>(p.dout);
-  const int64_t c0 = grad_col<NT, AL>(col0, 0);
-  for (int i0 = 0; i0 < n; i0 += U) {
-    if (key[i0 + 1] >= p.vocab) break;  // padding, sorted last
-    Raw8<T> raw[AL ? U : 1];
-    float one[AL ? 1 : U][8];
-    if (!AL) {
+  // adds position i's elements; writes the sum where its run ends, or the segment
+  auto add = [&](int i, const float* v) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] += v[e];
+    const bool goes_on = key[i + 2] == key[i + 1];
+    if (goes_on && i != in - 1) return;
+    float* parts = p.parts + seg * 2 * p.features;
+    if (began) {
+      grad_store<NT, AL>(parts, col0, p.features, acc, 1.f, false);
+    } else if (goes_on) {
+      grad_store<NT, AL>(parts + p.features, col0, p.features, acc, 1.f, false);
+      if (threadIdx.x == 0 && col0 == 0) p.spans[atomicAdd(p.nspans, 1u)] = (uint32_t)seg;
+    } else {
+      grad_store<NT, AL>(p.dtable + (int64_t)key[i + 1] * p.ldt, col0, p.features, acc, p.scale, p.accumulate);
+    }
+    began = false;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+  };
+  if constexpr (AL) {
+    constexpr int U = 8;  // rows in flight
+    const T* dout = static_cast<const T*>(p.dout);
+    const int64_t c0 = grad_col<NT, AL>(col0, 0);
+    for (int i0 = 0; i0 < n; i0 += U) {
+      Raw8<T> raw[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
+        raw[u] = i0 + u < n && c0 < p.features ? load_raw(dout + val[i0 + u] * p.ldo + c0) : zero_raw<T>();
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (i0 + u >= n) break;
+        float v[8];
+        unpack(raw[u], v);
+        add(i0 + u, v);
+      }
+    }
+  } else {
+    using Stage = RowStage<T, NT>;
+    const Stage stage(stage_smem, p);
+    const int cols = (int)min((int64_t)(8 * NT), p.features - col0);
+    stage.fetch(p, 0, val, min(n, Stage::kGroup), col0, cols);
+    for (int g = 0, i0 = 0; i0 < n; ++g, i0 += Stage::kGroup) {
+      const int next = i0 + Stage::kGroup;
+      stage.fetch(p, (g + 1) & 1, val + min(next, kSeg), max(0, min(n - next, Stage::kGroup)), col0, cols);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      __syncthreads();
+      for (int u = 0; u < Stage::kGroup && i0 + u < n; ++u) {
+        float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int64_t c = grad_col<NT, AL>(col0, e);
-          one[AL ? 0 : u][e] = i0 + u < n && key[i0 + u + 1] < p.vocab && c < p.features
-                                   ? to_float(dout[val[i0 + u] * p.ldo + c]) : 0.f;
+          const int c = e * NT + threadIdx.x;
+          v[e] = c < cols ? stage.read(p, g & 1, u, val[i0 + u], col0, c) : 0.f;
         }
-    }
-    if (AL) {
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        raw[AL ? u : 0] = i0 + u < n && key[i0 + u + 1] < p.vocab && c0 < p.features
-                              ? load_raw(dout + val[i0 + u] * p.ldo + c0) : zero_raw<T>();
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u;
-      if (i >= n || key[i + 1] >= p.vocab) break;
-      float v[8];
-      if (AL) {
-        unpack(raw[AL ? u : 0], v);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          v[e] = one[AL ? 0 : u][e];
-        }
+        add(i0 + u, v);
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += v[e];
-      const bool goes_on = key[i + 2] == key[i + 1];
-      if (goes_on && i != n - 1) continue;
-      float* parts = p.parts + seg * 2 * p.features;
-      if (began) {
-        grad_store<NT, AL>(parts, col0, p.features, acc, 1.f, false);
-      } else if (goes_on) {
-        grad_store<NT, AL>(parts + p.features, col0, p.features, acc, 1.f, false);
-        if (threadIdx.x == 0 && col0 == 0) p.spans[atomicAdd(p.nspans, 1u)] = (uint32_t)seg;
-      } else {
-        grad_store<NT, AL>(p.dtable + (int64_t)key[i + 1] * p.ldt, col0, p.features, acc, p.scale, p.accumulate);
-      }
-      began = false;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+      __syncthreads();  // the buffer is free again
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
 }
 
@@ -686,7 +755,11 @@ cudaError_t launch_sum(GradP p, bool al, int64_t segs, cudaStream_t s) {
     p.col_ctas = (int)((p.features + 8 * NT - 1) / (8 * NT));
     p.sum_ctas = segs * p.col_ctas;
     const int64_t grid = p.sum_ctas + (p.accumulate ? 0 : (p.vocab + p.zero_rows - 1) / p.zero_rows);
-    e = launch_after(al ? k_embed_sum<T, NT, true> : k_embed_sum<T, NT, false>, dim3((unsigned)grid), NT, 0, s, p);
+    const int bytes = al ? 0 : RowStage<T, NT>::kBytes;
+    if (bytes > 0)
+      e = cudaFuncSetAttribute(k_embed_sum<T, NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess)
+      e = launch_after(al ? k_embed_sum<T, NT, true> : k_embed_sum<T, NT, false>, dim3((unsigned)grid), NT, bytes, s, p);
   };
   if (p.features <= 256) go(std::integral_constant<int, 32>());
   else if (p.features <= 512) go(std::integral_constant<int, 64>());
