@@ -46,11 +46,27 @@ __device__ __forceinline__ int64_t load_id(const void* ids, int id64, int64_t t)
   return id64 ? __ldg(static_cast<const long long*>(ids) + t) : __ldg(static_cast<const int*>(ids) + t);
 }
 
+// N elements at once; the pointer is aligned to them (fp32: to 16 bytes at most).
+template <typename T, int N> struct alignas(sizeof(T) * N) Few { T v[N]; };
+template <typename T, int N>
+__device__ __forceinline__ void load_few(const T* p, float* v) {
+  const Few<T, N> f = *reinterpret_cast<const Few<T, N>*>(p);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = to_float(f.v[i]);
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_few(T* p, const float* v) {
+  Few<T, N> f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) f.v[i] = from_float<T>(v[i]);
+  *reinterpret_cast<Few<T, N>*>(p) = f;
+}
+
 // One item: VEC consecutive elements of an output row.
 constexpr int kLookups = 4;  // items of a thread in flight (of single elements twice as many)
 template <typename TI, typename TO, int VEC, typename I>
 __global__ void __launch_bounds__(kThreads) k_embed_lookup(const LookupP p, const RowDiv<I> row_of) {
-  constexpr int U = VEC == 1 ? 2 * kLookups : kLookups;
+  constexpr int U = VEC < 4 ? 2 * kLookups : kLookups;
   const I per_row = (I)(p.features / VEC), total = (I)(p.tokens * per_row);
   const I stride = (I)gridDim.x * kThreads;
   const TI* table = static_cast<const TI*>(p.table);
@@ -81,31 +97,46 @@ __global__ void __launch_bounds__(kThreads) k_embed_lookup(const LookupP p, cons
         store8(out + row[u] * p.ldo + col[u], v);
       }
     } else {
-      float v[U];
+      float v[U][VEC];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        v[u] = id[u] >= 0 && id[u] < p.vocab ? p.scale * to_float(table[id[u] * p.ldt + col[u]]) : 0.f;
+      for (int u = 0; u < U; ++u) {
+        const bool in = id[u] >= 0 && id[u] < p.vocab;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (i0 + u * stride < total) out[row[u] * p.ldo + col[u]] = from_float<TO>(v[u]);
+        for (int j = 0; j < VEC; ++j) v[u][j] = 0.f;
+        if (in) load_few<TI, VEC>(table + id[u] * p.ldt + col[u], v[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (i0 + u * stride >= total) continue;
+        const float f = id[u] >= 0 && id[u] < p.vocab ? p.scale : 0.f;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) v[u][j] *= f;
+        store_few<TO, VEC>(out + row[u] * p.ldo + col[u], v[u]);
+      }
     }
   }
 }
 
-template <typename TI, typename TO>
-void launch_lookup(const LookupP& p, bool vec, int sms, cudaStream_t s) {
-  const int64_t items = p.tokens * (vec ? p.features / 8 : p.features);
+template <typename TI, typename TO, int VEC>
+void launch_lookup(const LookupP& p, int sms, cudaStream_t s) {
+  const int64_t per_row = p.features / VEC, items = p.tokens * per_row;
   const int64_t want = (items + kThreads - 1) / kThreads, cap = (int64_t)sms * 8;
   const unsigned grid = (unsigned)(want < cap ? want : cap);
   // as the 8-bit form's: 32-bit indexes where they fit
-  const bool small = items + cap * kThreads * 2 * kLookups < (int64_t(1) << 31);
-  const int64_t per_row = vec ? p.features / 8 : p.features;
-  if (small) {
-    auto* kernel = vec ? k_embed_lookup<TI, TO, 8, uint32_t> : k_embed_lookup<TI, TO, 1, uint32_t>;
-    kernel<<<grid, kThreads, 0, s>>>(p, RowDiv<uint32_t>(per_row));
-  } else {
-    auto* kernel = vec ? k_embed_lookup<TI, TO, 8, int64_t> : k_embed_lookup<TI, TO, 1, int64_t>;
-    kernel<<<grid, kThreads, 0, s>>>(p, RowDiv<int64_t>(per_row));
+  if (items + cap * kThreads * 2 * kLookups < (int64_t(1) << 31))
+    k_embed_lookup<TI, TO, VEC, uint32_t><<<grid, kThreads, 0, s>>>(p, RowDiv<uint32_t>(per_row));
+  else
+    k_embed_lookup<TI, TO, VEC, int64_t><<<grid, kThreads, 0, s>>>(p, RowDiv<int64_t>(per_row));
+}
+
+// vec: elements that every row of both arrays can move at once.
+template <typename TI, typename TO>
+void launch_lookup(const LookupP& p, int vec, int sms, cudaStream_t s) {
+  switch (vec) {
+    case 8: launch_lookup<TI, TO, 8>(p, sms, s); break;
+    case 4: launch_lookup<TI, TO, 4>(p, sms, s); break;
+    case 2: launch_lookup<TI, TO, 2>(p, sms, s); break;
+    default: launch_lookup<TI, TO, 1>(p, sms, s);
   }
 }
 
@@ -727,8 +758,10 @@ dion_status lookup_impl(const dion_embed* a, void* stream) {
   if (a->tokens == 0) return DION_OK;
   const LookupP p{a->table, a->ids, a->out, a->ldt, a->ldo, a->tokens, a->vocab, a->features,
                   a->id_bytes == 8, a->scale};
-  const bool vec = a->features % 8 == 0 && rows_vector(a->table, a->ldt, ti) &&
-                   rows_vector(a->out, a->ldo, to);
+  int vec = 8;
+  while (vec > 1 && !(a->features % vec == 0 && a->ldt % vec == 0 && a->ldo % vec == 0 &&
+                      aligned_to(a->table, vec * ti) && aligned_to(a->out, vec * to)))
+    vec /= 2;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   auto from = [&](auto in) {
     using TI = decltype(in);
@@ -754,6 +787,9 @@ cudaError_t launch_sum(GradP p, bool al, int64_t segs, cudaStream_t s) {
     constexpr int NT = decltype(nt)::value;
     p.col_ctas = (int)((p.features + 8 * NT - 1) / (8 * NT));
     p.sum_ctas = segs * p.col_ctas;
+    // zeros: 512 bytes a thread, enough to pay for finding the CTA's rows in the list (the table
+    // of 32768 x 4096: 132 us, with 256 bytes 146)
+    p.zero_rows = (int)std::max<int64_t>(1, std::min<int64_t>(kZeroRows, NT * 512 / (4 * p.features)));
     const int64_t grid = p.sum_ctas + (p.accumulate ? 0 : (p.vocab + p.zero_rows - 1) / p.zero_rows);
     const int bytes = al ? 0 : RowStage<T, NT>::kBytes;
     if (bytes > 0)
@@ -843,8 +879,6 @@ dion_status embed_grad_impl(const dion_embed_grad* a, void* ws, size_t ws_bytes,
   p.scale = a->scale;
   p.accumulate = a->accumulate != 0;
   p.vec_table = a->features % 4 == 0 && rows_aligned16(a->dtable, a->ldt, 4);
-  // 128 KB of zeros to a CTA: enough to pay for finding its rows in the list
-  p.zero_rows = (int)std::max<int64_t>(1, std::min<int64_t>(kZeroRows, (128 << 10) / (4 * a->features)));
   const bool al = a->features % 8 == 0 && rows_vector(a->dtable, a->ldt, 4) && rows_vector(a->dout, a->ldo, es);
   DION_TRY(launch_status("k_embed_sum", a->dtype == DION_BF16   ? launch_sum<__nv_bfloat16>(p, al, g.segs, s)
                                         : a->dtype == DION_FP16 ? launch_sum<__half>(p, al, g.segs, s)

@@ -798,7 +798,9 @@ void by_width(int64_t d, F f) {
   if (d <= 256) f(std::integral_constant<int, 32>(), std::integral_constant<int, 1>());
   else if (d <= 512) f(std::integral_constant<int, 32>(), std::integral_constant<int, 2>());
   else if (d <= 1024) f(std::integral_constant<int, 64>(), std::integral_constant<int, 2>());
+  else if (d <= 1536) f(std::integral_constant<int, 96>(), std::integral_constant<int, 2>());
   else if (d <= 2048) f(std::integral_constant<int, 128>(), std::integral_constant<int, 2>());
+  else if (d <= 2560) f(std::integral_constant<int, 160>(), std::integral_constant<int, 2>());
   else if (d <= 4096) f(std::integral_constant<int, 256>(), std::integral_constant<int, 2>());
   else if (d <= 8192) f(std::integral_constant<int, 512>(), std::integral_constant<int, 2>());
   else f(std::integral_constant<int, 512>(), std::integral_constant<int, 4>());

@@ -207,12 +207,22 @@ __device__ __forceinline__ Unit unit_of(const WgradP& p, int u) {
   return t;
 }
 
+// Shared memory of a CTA: the rings, the barriers, and the epilogue's staging.
+template <int BN> struct Smem {
+  static constexpr int rings = SA * A_BYTES + SB * BK * BN + SQ * (Q_BYTES + 2 * BK * 4);
+  static constexpr int epilogue = rings + 512;  // the barriers in between
+  static constexpr int bytes = 1024 + epilogue + 8 * 32 * 9 * 4;
+  static_assert((2 * SQ + 2 * SB + 2 * SA + 5) * 8 + 16 <= 512, "the barriers");
+  static_assert(bytes <= 227 * 1024, "shared memory");
+};
+
 template <int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
     k_wgrad(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmD,
             const WgradP p) {
   constexpr int HB = BN / 2;               // columns of D that a CTA loads
   constexpr int B_BYTES = BK * HB * 2;
+  constexpr int kEpilogue = Smem<BN>::epilogue;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);     // the same offset in both CTAs
   uint8_t* sA = smem;
@@ -504,21 +514,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
         float* g = p.parts + ((int64_t)t.part * PM + rank * BM + row0 + place) * BN + col0;
 #pragma unroll
         for (int i = 0; i < HB; i += 8) store_sector(g + i, run + i);
-      } else if (row >= p.m) {
-        // a lane past the last feature writes nothing
       } else if (p.transposed) {
         // 32 lanes write 32 neighbouring features of one column
 #pragma unroll
         for (int i = 0; i < HB; ++i)
-          if (n0 + i < p.n) {
+          if (row < p.m && n0 + i < p.n) {
             float* g = p.out + (n0 + i) * p.ldg + row;
             *g = run[i] + (p.accumulate ? *g : 0.f);
           }
       } else {
-        float* g = p.out + row * p.ldg + n0;
+        float* g = p.out + min(row, p.m - 1) * p.ldg + n0;
 #pragma unroll
         for (int i = 0; i < HB; i += 8) {
-          if (p.vec && n0 + i + 7 < p.n) {
+          if (!p.vec) {
+            // rows that do not start on a sector: through shared memory, so that eight lanes write
+            // a row's eight columns instead of 32 lanes 32 rows
+            float* buf = reinterpret_cast<float*>(smem + kEpilogue) + ew * 32 * 9;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) buf[place * 9 + j] = run[i + j];
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int64_t r = t.m0 + rank * BM + row0 + 4 * k + (lane >> 3), col = n0 + i + (lane & 7);
+              if (r < p.m && col < p.n) {
+                float* to = p.out + r * p.ldg + col;
+                const float v = buf[(4 * k + (lane >> 3)) * 9 + (lane & 7)];
+                *to = v + (p.accumulate ? *to : 0.f);
+              }
+            }
+            __syncwarp();
+          } else if (row >= p.m) {
+            // a lane past the last feature writes nothing
+          } else if (n0 + i + 7 < p.n) {
             if (p.accumulate) {
               const float4 a = *reinterpret_cast<const float4*>(g + i), b = *reinterpret_cast<const float4*>(g + i + 4);
               run[i] += a.x; run[i + 1] += a.y; run[i + 2] += a.z; run[i + 3] += a.w;
@@ -704,10 +731,8 @@ dion_status check_source(const dion_grad_source& s, int i) {
 
 template <int BN>
 dion_status launch(const CUtensorMap& mq, const CUtensorMap& md, const WgradP& p, int sms, cudaStream_t s) {
-  constexpr size_t smem = 1024 + SA * A_BYTES + SB * BK * BN + SQ * (Q_BYTES + 2 * BK * 4) +
-                          (2 * SQ + 2 * SB + 2 * SA + 5) * 8 + 16;
-  const cudaError_t e = cudaFuncSetAttribute(k_wgrad<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)smem);
+  constexpr int smem = Smem<BN>::bytes;
+  const cudaError_t e = cudaFuncSetAttribute(k_wgrad<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return set_error(DION_ERR_CUDA, "k_wgrad: %s", cudaGetErrorString(e));
   const int64_t units = p.whole + (int64_t)p.tail * p.splits;
   const int64_t pairs = sms / 2;

@@ -69,6 +69,7 @@ NORM_SHAPES = [(1, 1, 0, 0), (3, 7, 0, 0), (5, 64, 0, 0), (4, 256, 0, 0), (9, 26
                # batches that are streamed, ragged in rows and columns
                (4801, 104, 0, 0), (5000, 264, 8, 0), (2500, 1016, 0, 0), (1201, 2048, 0, 0),
                (607, 4088, 8, 0), (301, 8192, 0, 0), (301, 8200, 0, 0),
+               (2000, 1280, 0, 0), (1500, 1531, 0, 0), (1000, 2552, 0, 0), (900, 2301, 0, 0),
                (607, 4095, 0, 0), (1203, 2041, 3, 5), (2500, 1015, 0, 1), (5000, 261, 0, 0),
                (4801, 99, 2, 3), (301, 8191, 1, 7)]
 
@@ -300,7 +301,7 @@ def test_act_special_blocks():
 # (tokens, m, n): one token, ragged tokens, tiles' borders, odd n (copied rows), many splits
 WGRAD_SHAPES = [(1, 8, 8), (1, 1, 1), (3, 40, 24), (63, 128, 64), (64, 128, 256), (65, 129, 65),
                 (255, 256, 128), (256, 32, 512), (257, 96, 264), (1000, 200, 72), (700, 130, 300),
-                (4099, 256, 128), (515, 1000, 777), (5000, 64, 8), (2048, 640, 1408), (300, 3, 1001), (517, 2000, 96), (700, 333, 257)]
+                (4099, 256, 128), (515, 1000, 777), (5000, 64, 8), (2048, 640, 1408), (300, 3, 1001), (517, 2000, 96), (700, 333, 257), (90, 770, 9665), (64, 500, 4099)]
 
 
 def _wgrad_inputs(t, m, n, seed, pad=0, shift=0):
@@ -392,7 +393,7 @@ def test_weight_grad_list_shares_a_workspace():
 # ------------------------------------------------------------------ embedding
 @pytest.mark.parametrize("table_t", ["fp32", "bf16", "fp16"])
 @pytest.mark.parametrize("out_t", ["bf16", "fp32", "fp16"])
-@pytest.mark.parametrize("t,v,d,pad,shift", [(1, 1, 1, 0, 0), (5, 7, 24, 0, 0), (300, 50, 136, 8, 0),
+@pytest.mark.parametrize("t,v,d,pad,shift", [(1, 1, 1, 0, 0), (5, 7, 24, 0, 0), (300, 50, 136, 8, 0), (90, 30, 36, 0, 0), (90, 30, 34, 0, 2), (200, 9, 52, 4, 4),
                                              (40, 9, 101, 0, 0), (33, 1000, 64, 3, 1)])
 def test_lookup(t, v, d, pad, shift, table_t, out_t):
     table = Rows(v, d, DT[table_t], pad, shift, fill=True, seed=1)
