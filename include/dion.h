@@ -500,7 +500,9 @@ typedef struct dion_grad_source {
 } dion_grad_source;
 
 /* Bytes of workspace for a list of sources (they take turns in it), from their shapes and d's
- * alignment; 0 when none is needed or a shape is not supported. */
+ * alignment; 0 when none is needed or a shape is not supported.  It holds partial sums, a copy
+ * of rows of d that do not start on 16 bytes, and, for gradients of many columns, A in bf16
+ * (2 bytes per element of A while the call runs). */
 size_t dion_weight_grad_workspace(const dion_grad_source* sources, int32_t nsources);
 
 /* Every gradient of the list, one after the other.  d_status (may be NULL): device int32,

@@ -6,7 +6,14 @@
 // [tokens, n] bf16 gradients of the layer's output, G fp32: what the optimizer step reads.
 //
 // A's values are exact in bf16 and so are the products in fp32; the only roundings are the
-// fp32 additions.  The contraction over the tokens runs on the tensor cores: a persistent pair
+// fp32 additions.  There are two kernels.  Where G has few columns, k_wgrad reads the 8-bit rows
+// and converts each tile on its way; where it has many, each feature's tile would be converted
+// once for every 256 columns, and the conversion's shared-memory traffic and power take a fifth of
+// the tensor cores' rate (1157 against 1449 TFLOP/s at m = 4096, n = 11008, 16384 tokens): there
+// A is first brought to bf16 rows in the workspace (dion_act_load) and k_wgrad_rows multiplies
+// those.
+//
+// The contraction over the tokens runs on the tensor cores: a persistent pair
 // of CTAs (a cluster, tcgen05 cta_group::2) owns 256 x BN tiles of G, each CTA 128 of the
 // features and half of the columns, and walks the tokens 64 at a time.  In each CTA
 //   warp 0        TMA producer of the 8-bit tile (64 tokens x 128 features)
@@ -20,8 +27,8 @@
 // The tensor cores' accumulation rounds toward zero, which adds up over thousands of MMAs,
 // so the tokens are cut into chunks of kChunk blocks, each accumulated from zero in TMEM
 // (two accumulators in turn), and the epilogue warps add the chunks in fp32 registers: over
-// 16384 like-signed products 3e-7 off (an fp32 product on CUDA cores 6e-7), at 1227 us for
-// m = 4096, n = 11008; chunks of 8 blocks 1.3e-7 at 1258 us, of 4 8e-8 at 1319 us.
+// 16384 like-signed products 3e-7 off (an fp32 product on CUDA cores 6e-7), in k_wgrad at
+// 1227 us for m = 4096, n = 11008; chunks of 8 blocks 1.3e-7 at 1258 us, of 4 8e-8 at 1319 us.
 // The tiles that do not fill a last round over all pairs (all of them, in a small matrix) are
 // also split over the tokens, so that every pair has a share; their partial sums go to the
 // workspace and a second kernel adds them in order.  Every wait is bounded.
@@ -207,6 +214,100 @@ __device__ __forceinline__ Unit unit_of(const WgradP& p, int u) {
   return t;
 }
 
+// The epilogue of one warp: 32 features and half of the tile's columns; `place` is the feature of
+// its TMEM lane.  Chunks are added in registers, the sum is written once.
+template <int BN>
+__device__ __forceinline__ void epilogue(const WgradP& p, float* staging, uint32_t tmem, uint64_t* tfull,
+                                         uint64_t* tempty, volatile int* abort, int ew, int lane, int place,
+                                         int rank, int pair, int pairs) {
+  constexpr int HB = BN / 2;
+  const int units = p.whole + p.tail * p.splits;
+  const int row0 = (ew & 3) * 32;
+  const int col0 = (ew >> 2) * HB;
+  int acc = 0;
+  uint32_t pacc = 0;
+  bool ok = true;
+  for (int u = pair; u < units && ok; u += pairs) {
+    const Unit t = unit_of<BN>(p, u);
+    float run[HB];
+#pragma unroll
+    for (int i = 0; i < HB; ++i) run[i] = 0.f;
+    for (int c0 = t.kb0; c0 < t.kb1; c0 += kChunk) {
+      const bool w = wait_bounded(tfull + acc, pacc, p.max_spins, abort);
+      if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+      tc_fence_after();
+      const uint32_t base = tmem + ((uint32_t)row0 << 16) + acc * BN + col0;
+#pragma unroll
+      for (int c = 0; c < HB; c += 8) {
+        float v[8];
+        tmem_ld8(base + c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) run[c + i] += v[i];
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_remote(first_cta(tempty + acc));
+      acc ^= 1;
+      if (acc == 0) pacc ^= 1;
+    }
+    if (!ok) break;
+    const int64_t row = t.m0 + rank * BM + row0 + place;
+    const int64_t n0 = t.n0 + col0;
+    if (t.part >= 0) {
+      float* g = p.parts + ((int64_t)t.part * PM + rank * BM + row0 + place) * BN + col0;
+#pragma unroll
+      for (int i = 0; i < HB; i += 8) store_sector(g + i, run + i);
+    } else if (p.transposed) {
+      // 32 lanes write 32 neighbouring features of one column
+#pragma unroll
+      for (int i = 0; i < HB; ++i)
+        if (row < p.m && n0 + i < p.n) {
+          float* g = p.out + (n0 + i) * p.ldg + row;
+          *g = run[i] + (p.accumulate ? *g : 0.f);
+        }
+    } else {
+      float* g = p.out + min(row, p.m - 1) * p.ldg + n0;
+#pragma unroll
+      for (int i = 0; i < HB; i += 8) {
+        if (!p.vec) {
+          // rows that do not start on a sector: through shared memory, so that eight lanes write
+          // a row's eight columns instead of 32 lanes 32 rows
+          float* buf = staging + ew * 32 * 9;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) buf[place * 9 + j] = run[i + j];
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int64_t r = t.m0 + rank * BM + row0 + 4 * k + (lane >> 3), col = n0 + i + (lane & 7);
+            if (r < p.m && col < p.n) {
+              float* to = p.out + r * p.ldg + col;
+              const float v = buf[(4 * k + (lane >> 3)) * 9 + (lane & 7)];
+              *to = v + (p.accumulate ? *to : 0.f);
+            }
+          }
+          __syncwarp();
+        } else if (row >= p.m) {
+          // a lane past the last feature writes nothing
+        } else if (n0 + i + 7 < p.n) {
+          if (p.accumulate) {
+            const float4 a = *reinterpret_cast<const float4*>(g + i), b = *reinterpret_cast<const float4*>(g + i + 4);
+            run[i] += a.x; run[i + 1] += a.y; run[i + 2] += a.z; run[i + 3] += a.w;
+            run[i + 4] += b.x; run[i + 5] += b.y; run[i + 6] += b.z; run[i + 7] += b.w;
+          }
+          store_sector(g + i, run + i);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (n0 + i + j < p.n) g[i + j] = run[i + j] + (p.accumulate ? g[i + j] : 0.f);
+        }
+      }
+    }
+    __syncwarp();  // the next unit's TMEM loads are warp-wide
+  }
+  if ((!ok || *abort) && lane == 0 && p.status) atomicOr(p.status, F_TIMEOUT);
+}
+
 // Shared memory of a CTA: the rings, the barriers, and the epilogue's staging.
 template <int BN> struct Smem {
   static constexpr int rings = SA * A_BYTES + SB * BK * BN + SQ * (Q_BYTES + 2 * BK * 4);
@@ -222,7 +323,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
             const WgradP p) {
   constexpr int HB = BN / 2;               // columns of D that a CTA loads
   constexpr int B_BYTES = BK * HB * 2;
-  constexpr int kEpilogue = Smem<BN>::epilogue;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);     // the same offset in both CTAs
   uint8_t* sA = smem;
@@ -475,93 +575,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   } else {
     // ---------------- epilogue: a warp owns 32 features and half of the tile's columns
     reg_inc<152>();
-    const int ew = warp - 4 - kGroups * kGroupWarps;
-    const int row0 = (ew & 3) * 32;
-    const int col0 = (ew >> 2) * HB;
     // TMEM lane to feature: the converters' order 0 2 1 3 of each four
     const int place = (lane & ~3) | ((lane & 1) << 1) | ((lane >> 1) & 1);
-    int acc = 0;
-    uint32_t pacc = 0;
-    bool ok = true;
-    for (int u = pair; u < units && ok; u += pairs) {
-      const Unit t = unit_of<BN>(p, u);
-      float run[HB];
-#pragma unroll
-      for (int i = 0; i < HB; ++i) run[i] = 0.f;
-      for (int c0 = t.kb0; c0 < t.kb1; c0 += kChunk) {
-        const bool w = wait_bounded(tfull + acc, pacc, p.max_spins, abort);
-        if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t base = tmem + ((uint32_t)row0 << 16) + acc * BN + col0;
-#pragma unroll
-        for (int c = 0; c < HB; c += 8) {
-          float v[8];
-          tmem_ld8(base + c, v);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 8; ++i) run[c + i] += v[i];
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_remote(first_cta(tempty + acc));
-        acc ^= 1;
-        if (acc == 0) pacc ^= 1;
-      }
-      if (!ok) break;
-      const int64_t row = t.m0 + rank * BM + row0 + place;
-      const int64_t n0 = t.n0 + col0;
-      if (t.part >= 0) {
-        float* g = p.parts + ((int64_t)t.part * PM + rank * BM + row0 + place) * BN + col0;
-#pragma unroll
-        for (int i = 0; i < HB; i += 8) store_sector(g + i, run + i);
-      } else if (p.transposed) {
-        // 32 lanes write 32 neighbouring features of one column
-#pragma unroll
-        for (int i = 0; i < HB; ++i)
-          if (row < p.m && n0 + i < p.n) {
-            float* g = p.out + (n0 + i) * p.ldg + row;
-            *g = run[i] + (p.accumulate ? *g : 0.f);
-          }
-      } else {
-        float* g = p.out + min(row, p.m - 1) * p.ldg + n0;
-#pragma unroll
-        for (int i = 0; i < HB; i += 8) {
-          if (!p.vec) {
-            // rows that do not start on a sector: through shared memory, so that eight lanes write
-            // a row's eight columns instead of 32 lanes 32 rows
-            float* buf = reinterpret_cast<float*>(smem + kEpilogue) + ew * 32 * 9;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) buf[place * 9 + j] = run[i + j];
-            __syncwarp();
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int64_t r = t.m0 + rank * BM + row0 + 4 * k + (lane >> 3), col = n0 + i + (lane & 7);
-              if (r < p.m && col < p.n) {
-                float* to = p.out + r * p.ldg + col;
-                const float v = buf[(4 * k + (lane >> 3)) * 9 + (lane & 7)];
-                *to = v + (p.accumulate ? *to : 0.f);
-              }
-            }
-            __syncwarp();
-          } else if (row >= p.m) {
-            // a lane past the last feature writes nothing
-          } else if (n0 + i + 7 < p.n) {
-            if (p.accumulate) {
-              const float4 a = *reinterpret_cast<const float4*>(g + i), b = *reinterpret_cast<const float4*>(g + i + 4);
-              run[i] += a.x; run[i + 1] += a.y; run[i + 2] += a.z; run[i + 3] += a.w;
-              run[i + 4] += b.x; run[i + 5] += b.y; run[i + 6] += b.z; run[i + 7] += b.w;
-            }
-            store_sector(g + i, run + i);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (n0 + i + j < p.n) g[i + j] = run[i + j] + (p.accumulate ? g[i + j] : 0.f);
-          }
-        }
-      }
-      __syncwarp();  // the next unit's TMEM loads are warp-wide
-    }
-    if ((!ok || *abort) && lane == 0 && p.status) atomicOr(p.status, F_TIMEOUT);
+    epilogue<BN>(p, reinterpret_cast<float*>(smem + Smem<BN>::epilogue), tmem, tfull, tempty, abort,
+                 warp - 4 - kGroups * kGroupWarps, lane, place, rank, pair, pairs);
   }
   tc_fence_before();
   __syncthreads();
@@ -569,6 +586,145 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, kCols);
+  }
+}
+
+// The same product from A already in bf16 (in the workspace): where a feature's tile meets many
+// tiles of columns, converting it once and for all costs less than once a tile.  Per CTA
+//   warp 0        TMA producer: A (64 tokens x 128 features) and half of the D tile
+//   warp 1        MMA issuer (one thread, in the pair's first CTA)
+//   warp 2        TMEM allocator
+//   warp 3        tells the issuer of each stage that has landed
+//   warps 4..11   epilogue
+constexpr int RBN = 256, RS = 6;                       // columns of a tile; stages
+constexpr int R_STAGE = A_BYTES + BK * RBN;            // A, and half of D's columns
+constexpr int RNT = 32 * 12;
+constexpr int kRowsEpilogue = RS * R_STAGE + 512;
+constexpr int kRowsSmem = 1024 + kRowsEpilogue + 8 * 32 * 9 * 4;
+static_assert((3 * RS + 5) * 8 + 16 <= 512 && kRowsSmem <= 227 * 1024, "shared memory");
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RNT, 1)
+    k_wgrad_rows(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmD,
+                 const WgradP p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + RS * R_STAGE);
+  uint64_t* empty = full + RS;
+  uint64_t* ready = empty + RS;             // used in the first CTA: both CTAs' stages have landed
+  uint64_t* tfull = ready + RS;
+  uint64_t* tempty = tfull + 2;             // used in the first CTA
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int units = p.whole + p.tail * p.splits;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < RS; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+      mbar_init(ready + s, 2);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull + a, 1);
+      mbar_init(tempty + a, 2 * 8);
+    }
+    mbar_init(drain, 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) tmem_alloc_pair(tmem_slot, 2 * RBN);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  grid_trigger();
+  if (warp == 0 && lane == 0) {
+    prefetch_map(&tmA);
+    prefetch_map(&tmD);
+    int stage = 0, used = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u = pair; u < units && ok; u += pairs) {
+      const Unit t = unit_of<RBN>(p, u);
+      for (int kb = t.kb0; kb < t.kb1; ++kb) {
+        if (!wait_bounded(empty + stage, phase ^ 1, p.max_spins, abort)) { ok = false; break; }
+        mbar_expect_tx(full + stage, R_STAGE);
+        uint8_t* to = smem + stage * R_STAGE;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          tma_load_2d(to + j * 8192, &tmA, full + stage, t.m0 + rank * BM + 64 * j, kb * BK);
+          tma_load_2d(to + A_BYTES + j * 8192, &tmD, full + stage, t.n0 + rank * (RBN / 2) + 64 * j, kb * BK);
+        }
+        if (used < RS) ++used;
+        if (++stage == RS) { stage = 0; phase ^= 1; }
+      }
+    }
+    if (*abort)  // let every load already issued land before the CTA goes away
+      for (int i = 0; i < used; ++i) {
+        stage = (stage + RS - 1) % RS;
+        if (stage == RS - 1) phase ^= 1;
+        wait_drain(full + stage, phase);
+      }
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    constexpr uint32_t idesc = idesc_bf16(PM, RBN, true, true);
+    int stage = 0, acc = 0;
+    uint32_t phase = 0, pacc = 0;
+    bool ok = true;
+    for (int u = pair; u < units && ok; u += pairs) {
+      const Unit t = unit_of<RBN>(p, u);
+      for (int c0 = t.kb0; c0 < t.kb1 && ok; c0 += kChunk) {
+        if (!wait_bounded(tempty + acc, pacc ^ 1, p.max_spins, abort)) { ok = false; break; }
+        tc_fence_after();
+        const int c1 = min(t.kb1, c0 + kChunk);
+        for (int kb = c0; kb < c1; ++kb) {
+          if (!wait_bounded(ready + stage, phase, p.max_spins, abort)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t ab = smem_u32(smem + stage * R_STAGE), bb = ab + A_BYTES;
+#pragma unroll
+          for (int k = 0; k < BK / 16; ++k)
+            mma_pair(tmem + acc * RBN, sw128_desc(ab + k * 2048, 8192, 1024),
+                     sw128_desc(bb + k * 2048, 8192, 1024), idesc, ((kb - c0) | k) != 0);
+          commit_pair(empty + stage);
+          if (++stage == RS) { stage = 0; phase ^= 1; }
+        }
+        if (!ok) break;
+        commit_pair(tfull + acc);
+        acc ^= 1;
+        if (acc == 0) pacc ^= 1;
+      }
+    }
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(drain))
+        : "memory");
+    wait_drain(drain, 0);
+  } else if (warp == 3 && lane == 0) {
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u = pair; u < units && ok; u += pairs) {
+      const Unit t = unit_of<RBN>(p, u);
+      for (int kb = t.kb0; kb < t.kb1; ++kb) {
+        if (!wait_bounded(full + stage, phase, p.max_spins, abort)) { ok = false; break; }
+        arrive_remote(first_cta(ready + stage));
+        if (++stage == RS) { stage = 0; phase ^= 1; }
+      }
+    }
+  } else if (warp >= 4) {
+    epilogue<RBN>(p, reinterpret_cast<float*>(smem + kRowsEpilogue), tmem, tfull, tempty, abort, warp - 4,
+                  lane, lane, rank, pair, pairs);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // neither CTA leaves while the other may still reach its memory
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 2 * RBN);
   }
 }
 
@@ -674,12 +830,17 @@ dion_status map2d(CUtensorMap* m, const void* base, CUtensorMapDataType type,
 // Pairs of SMs, and the fewest blocks in a split: below two, a pair's start and the join cost
 // more than the tokens.  Plans (and so workspace sizes) do not depend on the device asked.
 constexpr int kPairs = 74, kMinBlocks = 2;
+// A is converted beforehand (k_wgrad_rows) from this many columns and tokens on.  Converted first
+// and in the kernel, us: 16384 x 4096 x 11008 1020 and 1277, 8192 x 2048 x 2048 63 and 73,
+// 1024 x 4096 x 4096 54 and 63, 512 x 4096 x 11008 78 and 92; but 16384 x 4096 x 512 101 and 85,
+// 4096 x 1024 x 1024 29 and 27, 200 x 4096 x 4096 46 and 43.
+constexpr int64_t kRowsColumns = 1536, kRowsTokens = 512;
 
 struct GradPlan {
   int bn, tiles_m, whole, tail, splits, blocks, blocks_per_split;
-  bool pad;
+  bool pad, rows;       // D is copied into padded rows; A is converted beforehand
   int64_t ldd;          // of the padded copy
-  size_t parts_bytes, pad_bytes;
+  size_t parts_bytes, pad_bytes, rows_bytes;
 };
 
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
@@ -705,6 +866,8 @@ GradPlan plan_of(const dion_grad_source& s) {
   g.pad = !rows_aligned16(s.d, s.ldd, 2);
   g.ldd = (n + 7) / 8 * 8;
   g.parts_bytes = (size_t)g.tail * g.splits * PM * g.bn * 4;
+  g.rows = n >= kRowsColumns && s.kept.tokens >= kRowsTokens;
+  g.rows_bytes = g.rows ? up256((size_t)s.kept.tokens * kept_ld(m) * 2) : 0;
   g.pad_bytes = g.pad ? up256((size_t)s.kept.tokens * g.ldd * 2) : 0;
   return g;
 }
@@ -729,14 +892,15 @@ dion_status check_source(const dion_grad_source& s, int i) {
   return DION_OK;
 }
 
-template <int BN>
-dion_status launch(const CUtensorMap& mq, const CUtensorMap& md, const WgradP& p, int sms, cudaStream_t s) {
-  constexpr int smem = Smem<BN>::bytes;
-  const cudaError_t e = cudaFuncSetAttribute(k_wgrad<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+typedef void (*WgradKernel)(const CUtensorMap, const CUtensorMap, const WgradP);
+dion_status launch(WgradKernel kernel, int threads, int smem, const CUtensorMap& ma, const CUtensorMap& md,
+                   const WgradP& p, int sms, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return set_error(DION_ERR_CUDA, "k_wgrad: %s", cudaGetErrorString(e));
   const int64_t units = p.whole + (int64_t)p.tail * p.splits;
   const int64_t pairs = sms / 2;
-  k_wgrad<BN><<<(unsigned)(2 * (units < pairs ? units : pairs)), NT, smem, s>>>(mq, md, p);
+  kernel<<<(unsigned)(2 * (units < pairs ? units : pairs)), threads, smem, s>>>(ma, md, p);
   return launch_status("k_wgrad");
 }
 
@@ -752,7 +916,7 @@ dion_status one_grad(const dion_grad_source& src, int accumulate, char* ws, int3
   const void* d = src.d;
   int64_t ldd = src.ldd;
   if (g.pad) {
-    __nv_bfloat16* copy = reinterpret_cast<__nv_bfloat16*>(ws + g.parts_bytes);
+    __nv_bfloat16* copy = reinterpret_cast<__nv_bfloat16*>(ws + up256(g.parts_bytes));
     const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(src.d);
     if (tokens * (g.ldd / 8) + sms * 8 * 256 < (int64_t(1) << 31))
       k_wgrad_pad<uint32_t><<<sms * 8, 256, 0, s>>>(from, src.ldd, copy, g.ldd, tokens, n, RowDiv<uint32_t>(g.ldd / 8));
@@ -764,7 +928,14 @@ dion_status one_grad(const dion_grad_source& src, int accumulate, char* ws, int3
   }
   const int64_t ld = kept_ld(m);
   CUtensorMap mq, md;
-  DION_TRY(map2d(&mq, src.kept.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B,
+  if (g.rows) {
+    char* rows = ws + up256(g.parts_bytes) + g.pad_bytes;
+    dion_act_kept all = src.kept;
+    all.features = ld;  // whole blocks: rows of the copy are aligned
+    DION_TRY(dion_act_load(&all, rows, ld, DION_BF16, s));
+    DION_TRY(map2d(&mq, rows, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, (uint64_t)ld,
+                   (uint64_t)tokens, (uint64_t)ld * 2, 64, BK));
+  } else DION_TRY(map2d(&mq, src.kept.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B,
                  (uint64_t)ld, (uint64_t)tokens, (uint64_t)ld, BM, BK));
   DION_TRY(map2d(&md, d, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, (uint64_t)n,
                  (uint64_t)tokens, (uint64_t)ldd * 2, 64, BK));
@@ -789,7 +960,9 @@ dion_status one_grad(const dion_grad_source& src, int accumulate, char* ws, int3
   p.vec = aligned_to(src.G, 32) && src.ldg % 8 == 0;
   p.scale4 = p.ld_scale % 4 == 0 && aligned_to(p.scale, 4);
   p.max_spins = kMaxSpins;
-  const dion_status st = g.bn == 256 ? launch<256>(mq, md, p, sms, s) : launch<128>(mq, md, p, sms, s);
+  const dion_status st = g.rows        ? launch(k_wgrad_rows, RNT, kRowsSmem, mq, md, p, sms, s)
+                         : g.bn == 256 ? launch(k_wgrad<256>, NT, Smem<256>::bytes, mq, md, p, sms, s)
+                                       : launch(k_wgrad<128>, NT, Smem<128>::bytes, mq, md, p, sms, s);
   if (st != DION_OK || g.tail == 0) return st;
   return launch_status("k_wgrad_join", launch_after(k_wgrad_join, dim3((unsigned)(g.bn / 32), PM / 32, (unsigned)g.tail),
                                                     1024, 0, s, p, g.bn));
@@ -825,7 +998,7 @@ size_t dion_weight_grad_workspace(const dion_grad_source* sources, int32_t nsour
   for (int32_t i = 0; sources && i < nsources; ++i) {
     if (dion::check_shape(sources[i], i) != DION_OK) return 0;
     const dion::GradPlan g = dion::plan_of(sources[i]);
-    const size_t b = g.parts_bytes + g.pad_bytes;
+    const size_t b = dion::up256(g.parts_bytes) + g.pad_bytes + g.rows_bytes;
     most = b > most ? b : most;
   }
   return most;
