@@ -17,9 +17,12 @@
 // registers or the shared memory of the threads that own its columns in between.  A batch is
 // streamed: a fixed grid walks the rows, each thread fetching its own columns of the rows to
 // come into a ring of shared memory (cp.async; no thread reads another's slots, so the ring
-// needs no barrier) while it works on the current one, with its gains in registers.  A few
-// tokens, unaligned rows, and rows too wide for the ring are loaded directly, a row per CTA
-// (four rows, a warp each, up to 512 features).  The backward pass keeps each thread's column
+// needs no barrier) while it works on the current one, with its gains in registers.  Rows that
+// do not start on 16 bytes come as they lie and are read element by element (8192 x 4095 bf16
+// backward 148 us, 789 loaded directly).  Where no ring fits (fp32 backward, more than 8192
+// features) rows are loaded directly, a row per CTA, four rows a CTA up to 512 features.
+// 16384 x 4096 bf16: forward 85 us, kept in 8 bits as well 100, backward 142, which is 6.3, 6.0
+// and 5.7 TB/s of the 6.56 that a copy reaches.  The backward pass keeps each thread's column
 // sums over its rows; a second kernel adds the CTAs' sums in a fixed order, so results repeat
 // bit for bit.  All sums are fp32; only the stored rows are rounded.
 #include "operator.h"
@@ -64,7 +67,7 @@ struct NormGradP {
 
 // 1 / sqrt(v) to about half an ulp: one Newton step on the approximation.  With rsqrtf alone
 // (off by up to two) more of the 8-bit form's values fell on the wrong side of a tie: 1.5 times
-// the 64-bit distance that torch's fp32 form has; __frsqrt_rn does as well as the step and cost
+// the 64-bit distance of the plain fp32 form; __frsqrt_rn does as well as the step and cost
 // 5 us of 100 (16384 x 4096, kept), the step nothing.  An infinite v gives 0.
 __device__ __forceinline__ float inv_sqrt(float v) {
   const float r = rsqrtf(v);
@@ -815,23 +818,43 @@ cudaError_t allow_smem(const void* kernel, int bytes) {
                             : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-// Rows of the rings: three, two where three do not fit, none (the direct form) past that.
+// Rows of the rings: three, two where three do not fit, none (the direct form) past that.  fp32
+// forward on aligned rows takes the direct form, too: a piece is two 16-byte copies there, half a
+// sector each, and the stream of 8192 x 4096 ran at 133 us against 85 us.
 template <typename T, int NT, int VPT, int A, bool AL>
-int ring_stages() {
+constexpr int ring_stages() {
   constexpr int stage = Ring<T, NT, VPT, A, AL>::kStage * ctas_per_sm(NT);
-  return VPT > 2 ? 0 : 3 * stage <= kSmemMost ? 3 : 2 * stage <= kSmemMost ? 2 : 0;
+  if (VPT > 2 || (A == 2 && AL && sizeof(T) == 4)) return 0;
+  return 3 * stage <= kSmemMost ? 3 : 2 * stage <= kSmemMost ? 2 : 0;
 }
 
-// Launches the streaming kernel of A arrays, if its ring fits; false if it does not.
-template <typename T, int NT, int VPT, int A, bool AL, typename P>
-bool launch_stream(const P& p, unsigned grid, cudaStream_t s, cudaError_t* e, void (*three)(P), void (*two)(P)) {
-  const int stages = ring_stages<T, NT, VPT, A, AL>();
-  if (stages == 0) return false;
-  const int bytes = stages * Ring<T, NT, VPT, A, AL>::kStage;
-  auto* kernel = stages == 3 ? three : two;
-  *e = allow_smem((const void*)kernel, bytes);
-  if (*e == cudaSuccess) kernel<<<grid, cta_threads(NT), bytes, s>>>(p);
-  return true;
+template <typename K, typename P>
+cudaError_t launch_with(K* kernel, unsigned grid, int threads, int bytes, const P& p, cudaStream_t s) {
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), bytes);
+  if (e == cudaSuccess) kernel<<<grid, threads, bytes, s>>>(p);
+  return e;
+}
+
+template <typename T, int NT, int VPT, bool AL>
+cudaError_t launch_norm(const NormP& p, cudaStream_t s) {
+  constexpr int stages = ring_stages<T, NT, VPT, 2, AL>();
+  const int64_t rows = row_ctas(p.tokens, NT);
+  if constexpr (stages > 0)
+    return launch_with(k_norm_stream<T, NT, VPT, AL, stages>, (unsigned)std::min(rows, stream_ctas(NT)),
+                       cta_threads(NT), stages * Ring<T, NT, VPT, 2, AL>::kStage, p, s);
+  else
+    return launch_with(k_norm<T, NT, VPT, AL>, (unsigned)rows, cta_threads(NT), 0, p, s);
+}
+
+template <typename T, int NT, int VPT, bool AL>
+cudaError_t launch_grad(const NormGradP& p, unsigned grid, cudaStream_t s) {
+  constexpr int stages = ring_stages<T, NT, VPT, 4, AL>();
+  if constexpr (stages > 0)
+    return launch_with(k_norm_grad_stream<T, NT, VPT, AL, stages>, grid, cta_threads(NT),
+                       stages * Ring<T, NT, VPT, 4, AL>::kStage, p, s);
+  else
+    return launch_with(k_norm_grad<T, NT, VPT, AL>, grid, cta_threads(NT),
+                       VPT > 2 ? 2 * 8 * VPT * NT * 4 : 0, p, s);
 }
 
 template <typename T>
@@ -839,20 +862,7 @@ cudaError_t launch_norm(const NormP& p, bool al, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   by_width(p.features, [&](auto nt, auto vpt) {
     constexpr int NT = decltype(nt)::value, VPT = decltype(vpt)::value;
-    const int64_t rows = row_ctas(p.tokens, NT), fixed = stream_ctas(NT);
-    // fp32 forward takes the direct form: a thread's piece is two 16-byte copies there, half a
-    // sector each, and the stream of 8192 x 4096 ran at 133 us against 85 us
-    if constexpr (VPT <= 2) {
-      const unsigned grid = (unsigned)std::min(rows, fixed);
-      if ((sizeof(T) == 2 || !al) &&
-          (al ? launch_stream<T, NT, VPT, 2, true>(p, grid, s, &e, k_norm_stream<T, NT, VPT, true, 3>,
-                                                  k_norm_stream<T, NT, VPT, true, 2>)
-             : launch_stream<T, NT, VPT, 2, false>(p, grid, s, &e, k_norm_stream<T, NT, VPT, false, 3>,
-                                                   k_norm_stream<T, NT, VPT, false, 2>)))
-        return;
-    }
-    if (al) k_norm<T, NT, VPT, true><<<(unsigned)rows, cta_threads(NT), 0, s>>>(p);
-    else k_norm<T, NT, VPT, false><<<(unsigned)rows, cta_threads(NT), 0, s>>>(p);
+    e = al ? launch_norm<T, NT, VPT, true>(p, s) : launch_norm<T, NT, VPT, false>(p, s);
   });
   return e;
 }
@@ -862,17 +872,7 @@ cudaError_t launch_grad(const NormGradP& p, bool al, unsigned grid, cudaStream_t
   cudaError_t e = cudaSuccess;
   by_width(p.features, [&](auto nt, auto vpt) {
     constexpr int NT = decltype(nt)::value, VPT = decltype(vpt)::value;
-    if constexpr (VPT <= 2) {
-      if (al ? launch_stream<T, NT, VPT, 4, true>(p, grid, s, &e, k_norm_grad_stream<T, NT, VPT, true, 3>,
-                                                  k_norm_grad_stream<T, NT, VPT, true, 2>)
-             : launch_stream<T, NT, VPT, 4, false>(p, grid, s, &e, k_norm_grad_stream<T, NT, VPT, false, 3>,
-                                                   k_norm_grad_stream<T, NT, VPT, false, 2>))
-        return;
-    }
-    const int bytes = VPT > 2 ? 2 * 8 * VPT * NT * 4 : 0;
-    auto* kernel = al ? k_norm_grad<T, NT, VPT, true> : k_norm_grad<T, NT, VPT, false>;
-    e = allow_smem((const void*)kernel, bytes);
-    if (e == cudaSuccess) kernel<<<grid, cta_threads(NT), bytes, s>>>(p);
+    e = al ? launch_grad<T, NT, VPT, true>(p, grid, s) : launch_grad<T, NT, VPT, false>(p, grid, s);
   });
   return e;
 }

@@ -699,6 +699,41 @@ def test_two_lists_of_ids_in_turn_with_one_workspace():
         assert np.all(np.abs(_np(g) - go.embed_grad(ids.numpy(), _np(dout), v)) <= (hits[:, None] + 2) * U * mag)
 
 
+def test_every_operator_on_two_streams_at_once():
+    """Two sets of plans, each with its own buffers, on two streams in turn: both give what they
+    give alone."""
+    def plans(seed):
+        t, v, d, n = 3000, 700, 1032, 1600
+        r = lambda *s: torch.randn(*s, generator=_gen(seed)).cuda()  # noqa: E731
+        x, y, du = r(t, d).bfloat16(), r(t, d).bfloat16(), r(t, d).bfloat16()
+        ids = torch.randint(-1, v, (t,), generator=_gen(seed)).cuda()
+        dn, table = r(t, n).bfloat16(), r(v, d)
+        h, u, dx, dy, out = (torch.empty_like(x) for _ in range(5))
+        dw, dtable, G = torch.empty(d, device="cuda"), torch.empty(v, d, device="cuda"), torch.empty(d, n, device="cuda")
+        kept = dion.ActCheckpoint(t, d)
+        calls = [dion.NormPlan(x, y, h=h, u=u, post_norm=True, checkpoint=kept).forward,
+                 dion.NormGradPlan(x, y, du=du, dx=dx, dy=dy, post_norm=True, dpre_gain=dw).backward,
+                 dion.WeightGradPlan([kept], [dn], [G]).backward,
+                 dion.EmbedPlan(table, ids, out).lookup,
+                 dion.EmbedGradPlan(ids, du, dtable).backward]
+        return calls, [h, u, dx, dy, dw, G, out, dtable]
+
+    sets = [plans(1), plans(2)]
+    for calls, _ in sets:
+        for c in calls:
+            c()
+    torch.cuda.synchronize()
+    want = [[o.clone() for o in outs] for _, outs in sets]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(10):
+        for k in range(5):
+            for (calls, _), s in zip(sets, streams):
+                calls[k](stream=s)
+    torch.cuda.synchronize()
+    for (_, outs), w in zip(sets, want):
+        assert all(torch.equal(a, b) for a, b in zip(outs, w))
+
+
 def test_plans_refuse_tensors_that_do_not_fit():
     x = torch.zeros(4, 64, device="cuda")
     with pytest.raises(ValueError, match="must be"):
