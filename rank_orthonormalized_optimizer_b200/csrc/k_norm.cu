@@ -58,7 +58,7 @@ struct NormGradP {
   const void *h, *y, *du, *dh;
   void *dx, *dy;
   const float *pre, *post, *gate;
-  float* parts;  // [grid][2][features]
+  float* parts;  // [grid][2][part_ld(features)]
   int64_t ldh, ldy, lddu, lddh, lddx, lddy, tokens;
   int features;
   int post_norm;

@@ -830,6 +830,12 @@ dion_status map2d(CUtensorMap* m, const void* base, CUtensorMapDataType type,
 // Pairs of SMs, and the fewest blocks in a split: below two, a pair's start and the join cost
 // more than the tokens.  Plans (and so workspace sizes) do not depend on the device asked.
 constexpr int kPairs = 74, kMinBlocks = 2;
+// What a block of 64 tokens costs a pair, and what parts and their join cost: a launch, and a share
+// for each tile and each part, us.  The round is split where the blocks that it saves cost more.
+// Split and not: 512 x 1024 x 1024 20.5 and 15.1 us, 1024 x 1024 x 1024 22.1 and 18.5,
+// 1536 x 1024 x 1024 22.6 and 22.6, 2048 x 1024 x 1024 23.5 and 26.6, 3000 x 1024 x 1024 25.0 and
+// 32.8; 1024 x 256 x 256 14.4 and 18.5.
+constexpr double kBlockUs = 0.5, kJoinUs = 3, kJoinTileUs = 0.25, kJoinPartUs = 0.03;
 // A is converted beforehand (k_wgrad_rows) from this many columns and tokens on.  Converted first
 // and in the kernel, us: 16384 x 4096 x 11008 1020 and 1277, 8192 x 2048 x 2048 63 and 73,
 // 1024 x 4096 x 4096 54 and 63, 512 x 4096 x 11008 78 and 92; but 16384 x 4096 x 512 101 and 85,
@@ -858,8 +864,12 @@ GradPlan plan_of(const dion_grad_source& s) {
   want = std::min<int64_t>(want, g.blocks / kMinBlocks);
   g.splits = 1;
   if (want > 1) {
-    g.blocks_per_split = (int)((g.blocks + want - 1) / want);
-    g.splits = (g.blocks + g.blocks_per_split - 1) / g.blocks_per_split;
+    const int per = (int)((g.blocks + want - 1) / want), splits = (g.blocks + per - 1) / per;
+    const double join = kJoinUs + kJoinTileUs * tail + kJoinPartUs * tail * splits;
+    if ((g.blocks - per) * kBlockUs > join) {
+      g.blocks_per_split = per;
+      g.splits = splits;
+    }
   }
   g.tail = g.splits > 1 ? (int)tail : 0;
   g.whole = (int)(tiles - g.tail);

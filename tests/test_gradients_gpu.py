@@ -302,7 +302,8 @@ def test_act_special_blocks():
 WGRAD_SHAPES = [(1, 8, 8), (1, 1, 1), (3, 40, 24), (63, 128, 64), (64, 128, 256), (65, 129, 65),
                 (255, 256, 128), (256, 32, 512), (257, 96, 264), (1000, 200, 72), (700, 130, 300),
                 (4099, 256, 128), (515, 1000, 777), (5000, 64, 8), (2048, 640, 1408), (300, 3, 1001), (517, 2000, 96), (700, 333, 257), (90, 770, 9665), (64, 500, 4099),
-                (1024, 300, 2048), (2050, 520, 2501), (1500, 40, 5000)]
+                (1024, 300, 2048), (2050, 520, 2501), (1500, 40, 5000), (4096, 520, 6500),
+                (1100, 3400, 1400), (2050, 520, 1700)]
 
 
 def _wgrad_inputs(t, m, n, seed, pad=0, shift=0):
