@@ -74,27 +74,36 @@ __device__ __forceinline__ float inv_sqrt(float v) {
   return v < INFINITY ? fmaf(0.5f * r, fmaf(-v * r, r, 1.f), r) : r;
 }
 
-// Sum of N values over the NT threads that share a row (a warp, or the whole CTA).
+// Sums of N values over the NT threads that share a row (a warp, or the whole CTA).  The warps'
+// sums go through one half of red; the next call takes the other, whose readers were all done
+// before this call's barrier, so one barrier a call is enough.
+template <int NT> constexpr int red_floats() { return NT == 32 ? 1 : 2 * 4 * (NT / 32); }
 template <int NT, int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], float* red) {
+__device__ __forceinline__ void row_sum(float (&v)[N], float* red, int& half) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
   if (NT == 32) return;
-  constexpr int W = NT / 32;
-  const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
-  __syncthreads();  // the last sum's readers are done
-  if (l == 0)
+  constexpr int W = NT / 32, LD = N == 1 ? 1 : 4;
+  half ^= 1;
+  float* sums = red + half * 4 * W;
+  if ((threadIdx.x & 31) == 0)
 #pragma unroll
-    for (int i = 0; i < N; ++i) red[w * N + i] = v[i];
+    for (int i = 0; i < N; ++i) sums[(threadIdx.x >> 5) * LD + i] = v[i];
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = 0.f;
 #pragma unroll
-  for (int k = 0; k < W; ++k)
+  for (int k = 0; k < W; ++k) {
+    float a[LD];
+    if constexpr (LD == 4)
+      *reinterpret_cast<float4*>(a) = *reinterpret_cast<const float4*>(sums + 4 * k);
+    else
+      a[0] = sums[k];
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += red[k * N + i];
+    for (int i = 0; i < N; ++i) v[i] += a[i];
+  }
 }
 
 // Column of element e of this thread's row elements: groups of 8 where rows are 16-byte
@@ -214,7 +223,8 @@ __device__ __forceinline__ void keep_row(const NormP& p, int64_t row, int tid, c
 template <typename T, int NT, int VPT, bool AL>
 __global__ void __launch_bounds__(cta_threads(NT)) k_norm(const NormP p) {
   constexpr int E = 8 * VPT;
-  __shared__ float red[NT == 32 ? 1 : NT / 32];
+  __shared__ __align__(16) float red[red_floats<NT>()];
+  int half = 0;
   const int tid = NT == 32 ? threadIdx.x & 31 : threadIdx.x;
   const int64_t row = NT == 32 ? (int64_t)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
   if (row >= p.tokens) return;  // a whole warp, in the form without block barriers only
@@ -229,7 +239,7 @@ __global__ void __launch_bounds__(cta_threads(NT)) k_norm(const NormP p) {
       float ss[1] = {0.f};
 #pragma unroll
       for (int e = 0; e < E; ++e) ss[0] = fmaf(y[e], y[e], ss[0]);
-      row_sum<NT, 1>(ss, red);
+      row_sum<NT, 1>(ss, red, half);
       f *= inv_sqrt(fmaf(ss[0], p.inv_d, p.eps));
     }
 #pragma unroll
@@ -247,7 +257,7 @@ __global__ void __launch_bounds__(cta_threads(NT)) k_norm(const NormP p) {
 #pragma unroll
   for (int e = 0; e < E; ++e)
     if (column<NT, AL>(tid, e) < d) ss[0] = fmaf(h[e], h[e], ss[0]);
-  row_sum<NT, 1>(ss, red);
+  row_sum<NT, 1>(ss, red, half);
   const float r = inv_sqrt(fmaf(ss[0], p.inv_d, p.eps));
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
@@ -396,7 +406,8 @@ template <typename T, int NT, int VPT, bool AL, int STAGES>
 __global__ void __launch_bounds__(cta_threads(NT), ctas_per_sm(NT)) k_norm_stream(const NormP p) {
   constexpr int E = 8 * VPT, RPC = NT == 32 ? kWarpRows : 1;
   extern __shared__ uint4 ring_smem[];
-  __shared__ float red[NT == 32 ? 1 : NT / 32];
+  __shared__ __align__(16) float red[red_floats<NT>()];
+  int half = 0;
   const Ring<T, NT, VPT, 2, AL> ring(ring_smem);
   const int tid = NT == 32 ? threadIdx.x & 31 : threadIdx.x;
   const int d = p.features;
@@ -437,7 +448,7 @@ __global__ void __launch_bounds__(cta_threads(NT), ctas_per_sm(NT)) k_norm_strea
       if (p.post_norm) {
 #pragma unroll
         for (int e = 0; e < E; ++e) ss[0] = fmaf(y[e], y[e], ss[0]);
-        row_sum<NT, 1>(ss, red);
+        row_sum<NT, 1>(ss, red, half);
         f *= inv_sqrt(fmaf(ss[0], p.inv_d, p.eps));
         ss[0] = 0.f;
       }
@@ -452,7 +463,7 @@ __global__ void __launch_bounds__(cta_threads(NT), ctas_per_sm(NT)) k_norm_strea
 #pragma unroll
     for (int e = 0; e < E; ++e)
       if (column<NT, AL>(tid, e) < d) ss[0] = fmaf(h[e], h[e], ss[0]);
-    row_sum<NT, 1>(ss, red);
+    row_sum<NT, 1>(ss, red, half);
     finish_row<T, NT, VPT, AL>(p, row, tid, h, w, inv_sqrt(fmaf(ss[0], p.inv_d, p.eps)));
   }
   ring_wait<0>();
@@ -506,7 +517,8 @@ template <typename T, int NT, int VPT, bool AL, int STAGES>
 __global__ void __launch_bounds__(cta_threads(NT), ctas_per_sm(NT)) k_norm_grad_stream(const NormGradP p) {
   constexpr int E = 8 * VPT, RPC = NT == 32 ? kWarpRows : 1;
   extern __shared__ uint4 ring_smem[];
-  __shared__ float red[NT == 32 ? 1 : 3 * NT / 32];
+  __shared__ __align__(16) float red[red_floats<NT>()];
+  int half = 0;
   grid_trigger();  // a grid of one round, whose CTAs fill the SMs
   enum { H, DU, DH, Y };
   const Ring<T, NT, VPT, 4, AL> ring(ring_smem);
@@ -539,13 +551,10 @@ __global__ void __launch_bounds__(cta_threads(NT), ctas_per_sm(NT)) k_norm_grad_
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) apre[e] = apost[e] = 0.f;
-  int stage = 0;
-  for (int64_t row = first; row < p.tokens; row += step) {
-    ring_wait<STAGES - 2>();
-    ring.arrived();
-    // the slots read in the last round take the next row
-    fetch(row + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
-    float sum[3] = {0.f, 0.f, 0.f};
+  // the row's sums for both norms, this thread's share
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  auto statistics = [&](int64_t row, int stage) {
+    sum[0] = sum[1] = sum[2] = 0.f;
     if (p.du)
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
@@ -566,7 +575,16 @@ __global__ void __launch_bounds__(cta_threads(NT), ctas_per_sm(NT)) k_norm_grad_
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum[2] = fmaf(y[j], y[j], sum[2]);
       }
-    row_sum<NT, 3>(sum, red);
+  };
+  ring_wait<STAGES - 2>();
+  ring.arrived();
+  if (first < p.tokens) statistics(first, 0);
+  row_sum<NT, 4>(sum, red, half);
+  int stage = 0;
+  for (int64_t row = first; row < p.tokens; row += step) {
+    if (!AL) ring.arrived();  // all have read the last row
+    // the slots read in the last round take the next row
+    fetch(row + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
     float g[E];
     const float r = inv_sqrt(fmaf(sum[0], p.inv_d, p.eps));
     const float m1 = sum[1] * r * p.inv_d;
@@ -592,9 +610,9 @@ __global__ void __launch_bounds__(cta_threads(NT), ctas_per_sm(NT)) k_norm_grad_
       }
     }
     if (p.dx) store_row<T, NT, VPT, AL>(static_cast<T*>(p.dx) + row * p.lddx, tid, d, g);
-    if (p.y) {
-      const float ry = p.post_norm ? inv_sqrt(fmaf(sum[2], p.inv_d, p.eps)) : 1.f;
-      float dot[1] = {0.f};
+    const float ry = p.post_norm ? inv_sqrt(fmaf(sum[2], p.inv_d, p.eps)) : 1.f;
+    sum[3] = 0.f;
+    if (p.y)
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
         float y[8];
@@ -605,12 +623,18 @@ __global__ void __launch_bounds__(cta_threads(NT), ctas_per_sm(NT)) k_norm_grad_
           const float yn = y[j] * ry;
           apost[e] = fmaf(g[e], yn, apost[e]);
           g[e] *= c[e];
-          dot[0] = fmaf(g[e], yn, dot[0]);
+          sum[3] = fmaf(g[e], yn, sum[3]);
         }
       }
+    // this row's last sum and the next row's first ones share a barrier
+    const int next = stage + 1 == STAGES ? 0 : stage + 1;
+    ring_wait<STAGES - 2>();
+    ring.arrived();
+    if (row + step < p.tokens) statistics(row + step, next);
+    row_sum<NT, 4>(sum, red, half);
+    if (p.dy) {
       if (p.post_norm) {
-        row_sum<NT, 1>(dot, red);
-        const float m2 = dot[0] * p.inv_d;
+        const float m2 = sum[3] * p.inv_d;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
           float y[8];
@@ -619,9 +643,9 @@ __global__ void __launch_bounds__(cta_threads(NT), ctas_per_sm(NT)) k_norm_grad_
           for (int j = 0; j < 8; ++j) g[8 * k + j] = ry * fmaf(-y[j] * ry, m2, g[8 * k + j]);
         }
       }
-      if (p.dy) store_row<T, NT, VPT, AL>(static_cast<T*>(p.dy) + row * p.lddy, tid, d, g);
+      store_row<T, NT, VPT, AL>(static_cast<T*>(p.dy) + row * p.lddy, tid, d, g);
     }
-    if (++stage == STAGES) stage = 0;
+    stage = next;
   }
   ring_wait<0>();
   write_parts<NT, VPT, AL>(p, tid, apre, apost);
@@ -635,7 +659,8 @@ __global__ void __launch_bounds__(cta_threads(NT)) k_norm_grad(const NormGradP p
   constexpr int RPC = NT == 32 ? kWarpRows : 1;
   constexpr bool WIDE = VPT > 2;
   extern __shared__ float wide[];  // [2][E][NT]
-  __shared__ float red[NT == 32 ? 1 : 3 * NT / 32];
+  __shared__ __align__(16) float red[red_floats<NT>()];
+  int half = 0;
   const int tid = NT == 32 ? threadIdx.x & 31 : threadIdx.x;
   const int sub = NT == 32 ? threadIdx.x >> 5 : 0;
   const int d = p.features;
@@ -685,7 +710,7 @@ __global__ void __launch_bounds__(cta_threads(NT)) k_norm_grad(const NormGradP p
     if (p.y && p.post_norm)
 #pragma unroll
       for (int e = 0; e < E; ++e) sum[2] = fmaf(y[e], y[e], sum[2]);
-    row_sum<NT, 3>(sum, red);
+    row_sum<NT, 3>(sum, red, half);
     if (p.du) {
       const float r = inv_sqrt(fmaf(sum[0], p.inv_d, p.eps));
       const float m1 = sum[1] * r * p.inv_d;
@@ -721,7 +746,7 @@ __global__ void __launch_bounds__(cta_threads(NT)) k_norm_grad(const NormGradP p
       }
     }
     if (p.post_norm) {
-      row_sum<NT, 1>(dot, red);
+      row_sum<NT, 1>(dot, red, half);
       const float m2 = dot[0] * p.inv_d;
 #pragma unroll
       for (int e = 0; e < E; ++e) g[e] = ry * fmaf(-y[e], m2, g[e]);
@@ -818,14 +843,15 @@ cudaError_t allow_smem(const void* kernel, int bytes) {
                             : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-// Rows of the rings: three, two where three do not fit, none (the direct form) past that.  fp32
+// Rows of the rings: three, two of the forward pass where three do not fit, none (the direct form)
+// past that; the backward pass has two rows in work and one on its way.  fp32
 // forward on aligned rows takes the direct form, too: a piece is two 16-byte copies there, half a
 // sector each, and the stream of 8192 x 4096 ran at 133 us against 85 us.
 template <typename T, int NT, int VPT, int A, bool AL>
 constexpr int ring_stages() {
   constexpr int stage = Ring<T, NT, VPT, A, AL>::kStage * ctas_per_sm(NT);
   if (VPT > 2 || (A == 2 && AL && sizeof(T) == 4)) return 0;
-  return 3 * stage <= kSmemMost ? 3 : 2 * stage <= kSmemMost ? 2 : 0;
+  return 3 * stage <= kSmemMost ? 3 : 2 * stage <= kSmemMost && A == 2 ? 2 : 0;
 }
 
 template <typename K, typename P>
