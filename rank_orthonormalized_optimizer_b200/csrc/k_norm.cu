@@ -19,10 +19,12 @@
 // come into a ring of shared memory (cp.async; no thread reads another's slots, so the ring
 // needs no barrier) while it works on the current one, with its gains in registers.  Rows that
 // do not start on 16 bytes come as they lie and are read element by element (8192 x 4095 bf16
-// backward 148 us, 789 loaded directly).  Where no ring fits (fp32 backward, more than 8192
+// backward 152 us, 789 loaded directly).  Where no ring fits (fp32 backward, more than 8192
 // features) rows are loaded directly, a row per CTA, four rows a CTA up to 512 features.
-// 16384 x 4096 bf16: forward 85 us, kept in 8 bits as well 100, backward 142, which is 6.3, 6.0
-// and 5.7 TB/s of the 6.56 that a copy reaches.  The backward pass keeps each thread's column
+// 16384 x 4096 bf16: forward 86 us, kept in 8 bits as well 97, backward 129, which is 6.2 TB/s of
+// the 6.56 that a copy reaches.  A row's barriers cost most where a CTA has its SM for itself, so
+// the backward pass adds a row's last sum and the next row's first ones in one (8192 x 8192 142 us,
+// with a sum for each and two barriers a sum 187; 16384 x 4096 143).  The backward pass keeps each thread's column
 // sums over its rows; a second kernel adds the CTAs' sums in a fixed order, so results repeat
 // bit for bit.  All sums are fp32; only the stored rows are rounded.
 #include "operator.h"
@@ -820,7 +822,8 @@ __global__ void __launch_bounds__(kGainThreads) k_norm_gains(const GainP p) {
 }
 
 // Threads of a row and 8-element pieces of a thread, by the features: a warp up to 512, then
-// the smallest CTA that holds the row in two pieces a thread, four at the widest.
+// the smallest CTA that holds the row in two pieces a thread, four at the widest.  (8192 x 5120
+// bf16: 71 and 112 us forward and backward with 320 threads, 78 and 134 with 512.)
 template <typename F>
 void by_width(int64_t d, F f) {
   if (d <= 256) f(std::integral_constant<int, 32>(), std::integral_constant<int, 1>());
@@ -830,6 +833,8 @@ void by_width(int64_t d, F f) {
   else if (d <= 2048) f(std::integral_constant<int, 128>(), std::integral_constant<int, 2>());
   else if (d <= 2560) f(std::integral_constant<int, 160>(), std::integral_constant<int, 2>());
   else if (d <= 4096) f(std::integral_constant<int, 256>(), std::integral_constant<int, 2>());
+  else if (d <= 5120) f(std::integral_constant<int, 320>(), std::integral_constant<int, 2>());
+  else if (d <= 6144) f(std::integral_constant<int, 384>(), std::integral_constant<int, 2>());
   else if (d <= 8192) f(std::integral_constant<int, 512>(), std::integral_constant<int, 2>());
   else f(std::integral_constant<int, 512>(), std::integral_constant<int, 4>());
 }
@@ -843,15 +848,16 @@ cudaError_t allow_smem(const void* kernel, int bytes) {
                             : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-// Rows of the rings: three, two of the forward pass where three do not fit, none (the direct form)
-// past that; the backward pass has two rows in work and one on its way.  fp32
-// forward on aligned rows takes the direct form, too: a piece is two 16-byte copies there, half a
-// sector each, and the stream of 8192 x 4096 ran at 133 us against 85 us.
+// Rows of the rings, none where they do not fit (the direct form).  Backward, two rows are in work
+// and one or two on their way; forward one is in work, and more than two on their way gain nothing.
+// fp32 forward on aligned rows takes the direct form, too: a piece is two 16-byte copies there, half
+// a sector each, and the stream of 8192 x 4096 ran at 133 us against 85 us.
 template <typename T, int NT, int VPT, int A, bool AL>
 constexpr int ring_stages() {
   constexpr int stage = Ring<T, NT, VPT, A, AL>::kStage * ctas_per_sm(NT);
   if (VPT > 2 || (A == 2 && AL && sizeof(T) == 4)) return 0;
-  return 3 * stage <= kSmemMost ? 3 : 2 * stage <= kSmemMost && A == 2 ? 2 : 0;
+  constexpr int least = A == 4 ? 3 : 2, most = A == 4 ? 4 : 3, fit = kSmemMost / stage;
+  return fit < least ? 0 : fit < most ? fit : most;
 }
 
 template <typename K, typename P>

@@ -69,6 +69,7 @@ NORM_SHAPES = [(1, 1, 0, 0), (3, 7, 0, 0), (5, 64, 0, 0), (4, 256, 0, 0), (9, 26
                # batches that are streamed, ragged in rows and columns
                (4801, 104, 0, 0), (5000, 264, 8, 0), (2500, 1016, 0, 0), (1201, 2048, 0, 0),
                (607, 4088, 8, 0), (301, 8192, 0, 0), (301, 8200, 0, 0),
+               (700, 5120, 0, 0), (450, 4104, 8, 0), (450, 6144, 0, 0), (301, 6001, 0, 0), (301, 5122, 0, 1),
                (2000, 1280, 0, 0), (1500, 1531, 0, 0), (1000, 2552, 0, 0), (900, 2301, 0, 0),
                (607, 4095, 0, 0), (1203, 2041, 3, 5), (2500, 1015, 0, 1), (5000, 261, 0, 0),
                (4801, 99, 2, 3), (301, 8191, 1, 7)]
