@@ -44,6 +44,12 @@ constexpr int kSmemMost = 226 * 1024;    // of the rings of one SM's CTAs
 // Threads of a CTA, and CTAs of a streaming grid on an SM (512 threads of 128 registers).
 constexpr int cta_threads(int nt) { return nt == 32 ? 32 * kWarpRows : nt; }
 constexpr int ctas_per_sm(int nt) { return cta_threads(nt) > 512 ? 1 : 512 / cta_threads(nt); }
+// The backward stream's: from two warps on those that make up 384 threads, each with longer rings
+// and fewer parts (16384 x 1024 bf16 41.7 us, with 512 threads 42.9; x 2048 71 and 74).
+constexpr int grad_ctas_per_sm(int nt) {
+  const int most = ctas_per_sm(nt), want = (384 + nt - 1) / nt;
+  return nt == 32 || most < want ? most : want;
+}
 
 struct NormP {
   const void *x, *y;
@@ -516,7 +522,7 @@ __device__ __forceinline__ void write_parts(const NormGradP& p, int tid, float* 
 }
 
 template <typename T, int NT, int VPT, bool AL, int STAGES>
-__global__ void __launch_bounds__(cta_threads(NT), ctas_per_sm(NT)) k_norm_grad_stream(const NormGradP p) {
+__global__ void __launch_bounds__(cta_threads(NT), grad_ctas_per_sm(NT)) k_norm_grad_stream(const NormGradP p) {
   constexpr int E = 8 * VPT, RPC = NT == 32 ? kWarpRows : 1;
   extern __shared__ uint4 ring_smem[];
   __shared__ __align__(16) float red[red_floats<NT>()];
@@ -854,7 +860,7 @@ cudaError_t allow_smem(const void* kernel, int bytes) {
 // a sector each, and the stream of 8192 x 4096 ran at 133 us against 85 us.
 template <typename T, int NT, int VPT, int A, bool AL>
 constexpr int ring_stages() {
-  constexpr int stage = Ring<T, NT, VPT, A, AL>::kStage * ctas_per_sm(NT);
+  constexpr int stage = Ring<T, NT, VPT, A, AL>::kStage * (A == 4 ? grad_ctas_per_sm(NT) : ctas_per_sm(NT));
   if (VPT > 2 || (A == 2 && AL && sizeof(T) == 4)) return 0;
   constexpr int least = A == 4 ? 3 : 2, most = A == 4 ? 4 : 3, fit = kSmemMost / stage;
   return fit < least ? 0 : fit < most ? fit : most;
@@ -879,12 +885,13 @@ cudaError_t launch_norm(const NormP& p, cudaStream_t s) {
 }
 
 template <typename T, int NT, int VPT, bool AL>
-cudaError_t launch_grad(const NormGradP& p, unsigned grid, cudaStream_t s) {
+cudaError_t launch_grad(const NormGradP& p, unsigned& grid, cudaStream_t s) {
   constexpr int stages = ring_stages<T, NT, VPT, 4, AL>();
-  if constexpr (stages > 0)
+  if constexpr (stages > 0) {
+    grid = std::min(grid, (unsigned)(kSms * grad_ctas_per_sm(NT)));
     return launch_with(k_norm_grad_stream<T, NT, VPT, AL, stages>, grid, cta_threads(NT),
                        stages * Ring<T, NT, VPT, 4, AL>::kStage, p, s);
-  else
+  } else
     return launch_with(k_norm_grad<T, NT, VPT, AL>, grid, cta_threads(NT),
                        VPT > 2 ? 2 * 8 * VPT * NT * 4 : 0, p, s);
 }
@@ -900,7 +907,7 @@ cudaError_t launch_norm(const NormP& p, bool al, cudaStream_t s) {
 }
 
 template <typename T>
-cudaError_t launch_grad(const NormGradP& p, bool al, unsigned grid, cudaStream_t s) {
+cudaError_t launch_grad(const NormGradP& p, bool al, unsigned& grid, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   by_width(p.features, [&](auto nt, auto vpt) {
     constexpr int NT = decltype(nt)::value, VPT = decltype(vpt)::value;
@@ -1036,7 +1043,7 @@ dion_status norm_grad_impl(const dion_norm_grad* a, void* ws, size_t ws_bytes, v
   int sms = 0;
   DION_TRY(check_sm100(&sms));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const unsigned grid = grad_grid(a->tokens, a->features);
+  unsigned grid = grad_grid(a->tokens, a->features);  // the parts that the workspace holds, at most
   if (grid > 0) {
     NormGradP p{};
     p.h = a->h; p.y = a->y; p.du = a->du; p.dh = a->dh; p.dx = a->dx; p.dy = a->dy;
