@@ -73,13 +73,15 @@ struct NormGradP {
   float eps, s, inv_d;
 };
 
-// 1 / sqrt(v) to about half an ulp: one Newton step on the approximation.  With rsqrtf alone
-// (off by up to two) more of the 8-bit form's values fell on the wrong side of a tie: 1.5 times
-// the 64-bit distance of the plain fp32 form; __frsqrt_rn does as well as the step and cost
-// 5 us of 100 (16384 x 4096, kept), the step nothing.  An infinite v gives 0.
+// 1 / sqrt(v) to about half an ulp: one Newton step on the approximation, with v r in two parts.
+// An error here is a row's, and moves values of the 8-bit form across ties: with rsqrtf alone (off
+// by up to two ulps) it was 1.5 times as far from the 64-bit result as the plain fp32 form, with
+// the step 0.91 times (mean of six draws of 8192 x 4096, some 40 values each; v r in one part
+// 0.97).  __frsqrt_rn does as well and cost 5 us of 100 (16384 x 4096, kept), the step nothing.
+// An infinite v gives 0.
 __device__ __forceinline__ float inv_sqrt(float v) {
-  const float r = rsqrtf(v);
-  return v < INFINITY ? fmaf(0.5f * r, fmaf(-v * r, r, 1.f), r) : r;
+  const float r = rsqrtf(v), p = v * r, low = fmaf(v, r, -p);
+  return v < INFINITY ? fmaf(0.5f * r, fmaf(-low, r, fmaf(-p, r, 1.f)), r) : r;
 }
 
 // Sums of N values over the NT threads that share a row (a warp, or the whole CTA).  The warps'
