@@ -104,11 +104,45 @@ def _dtype(t) -> int:
     return code
 
 
+class _Owned:
+    """Device memory that a plan allocates, on the stream that is current then (the home stream).
+    Once freed, the caching allocator gives it to the home stream's next allocation at once, so
+    every other stream that uses it is named to the allocator (record_stream), which then waits
+    for that stream's work; and that stream waits for what the home stream had enqueued when the
+    memory was handed out: the work of its last owner, and the zeroing of status words."""
+
+    def __init__(self, *tensors):
+        import torch
+        self.tensors = tensors
+        home = torch.cuda.current_stream(tensors[0].device)
+        self.streams, self._made = {home.cuda_stream}, None
+        # (made inside a capture, the memory is the graph's, whose streams all fork from this one)
+        if not _capturing(home):
+            self._made = torch.cuda.Event()
+            self._made.record(home)
+
+    def use(self, stream):
+        for t in self.tensors:
+            t.record_stream(stream)
+        # an event of before a capture cannot be waited for inside it; the replays come after the
+        # work before the capture, and the next call outside waits
+        if not _capturing(stream):
+            if self._made is not None:
+                stream.wait_event(self._made)
+            self.streams.add(stream.cuda_stream)
+
+
+def _capturing(stream) -> bool:
+    import torch
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 class _Bound:
     """Tensors of one plan: checked, kept alive, all on one device."""
 
     def __init__(self):
-        self._device, self._keep = None, []
+        self._device, self._keep, self._owned = None, [], []
 
     def _tensor(self, name, t, dtype=None):
         import torch
@@ -145,16 +179,31 @@ class _Bound:
             raise ValueError(f"{name} must be a contiguous vector of {n}")
         return t.data_ptr()
 
-    def _workspace(self, workspace, nbytes):
-        """(pointer, bytes) of the caller's workspace, or of one that the plan allocates."""
+    def _workspace(self, workspace, nbytes, status_words=0):
+        """(pointer, bytes) of the caller's workspace, or of one that the plan allocates; and the
+        plan's zeroed status words."""
         import torch
+        own = []
         if workspace is None:
             workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=self._device)
+            own.append(workspace)
         self._tensor("workspace", workspace, torch.uint8)
         if workspace.numel() < nbytes or not workspace.is_contiguous():
             raise ValueError(f"workspace must be {nbytes} contiguous bytes, got {workspace.numel()}")
         self.workspace_bytes = nbytes
-        return c_void_p(workspace.data_ptr()), workspace.numel()
+        status = None
+        if status_words:
+            status = torch.zeros(status_words, dtype=torch.int32, device=self._device)
+            own.append(status)
+        if own:
+            self._owned.append(_Owned(*own))
+        return c_void_p(workspace.data_ptr()), workspace.numel(), status
+
+    def _checkpoint(self, k):
+        """An ActCheckpoint that the plan reads or writes."""
+        self._tensor("checkpoint", k.q)
+        self._keep.append(k)
+        self._owned += [o for o in k._owned if o not in self._owned]
 
     def _stream(self, stream):
         import torch
@@ -162,9 +211,12 @@ class _Bound:
         if device != self._device.index:
             raise ValueError(f"the plan's tensors are on {self._device}, the current device is "
                              f"cuda:{device}")
-        if stream is None:      # the handle alone: a Stream object takes longer than the launch
-            return torch._C._cuda_getCurrentRawStream(device)
-        return stream.cuda_stream
+        # the handle alone: a Stream object takes longer than the launch
+        raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+        for owned in self._owned:
+            if raw not in owned.streams:
+                owned.use(torch.cuda.current_stream(device) if stream is None else stream)
+        return raw
 
 
 # ------------------------------------------------------------------ activations in 8 bits
@@ -180,10 +232,13 @@ class ActCheckpoint(_Bound):
             raise ValueError("tokens >= 0 and features >= 1 expected")
         self.tokens, self.features = int(tokens), int(features)
         ld = -(-self.features // ACT_BLOCK) * ACT_BLOCK
+        own = []
         if q is None:
             q = torch.empty(self.tokens, ld, dtype=torch.uint8, device=device or "cuda")
+            own.append(q)
         if scale is None:
             scale = torch.empty(self.tokens, ld // ACT_BLOCK, dtype=torch.uint8, device=q.device)
+            own.append(scale)
         for name, t, shape in (("q", q, (self.tokens, ld)),
                                ("scale", scale, (self.tokens, ld // ACT_BLOCK))):
             self._tensor(name, t, torch.uint8)
@@ -192,6 +247,8 @@ class ActCheckpoint(_Bound):
         self.q, self.scale = q, scale
         self.args = ActKept(q.data_ptr(), scale.data_ptr(), self.tokens, self.features)
         self._keep, self._shape = [q, scale], (self.tokens, self.features)
+        if own:
+            self._owned.append(_Owned(*own))
         self._ref = ctypes.byref(self.args)
         _dtype_codes()
 
@@ -232,8 +289,7 @@ def _sources(bound, checkpoints, dys, transposed):
     for i, (k, d) in enumerate(zip(checkpoints, dys)):
         if not isinstance(k, ActCheckpoint):
             raise ValueError(f"matrix {i}: an ActCheckpoint is expected")
-        bound._tensor("checkpoint", k.q)
-        bound._keep.append(k)
+        bound._checkpoint(k)
         if getattr(d, "ndim", 0) != 2:
             raise ValueError(f"matrix {i}: dy must be [tokens, n]")
         arr[i].kept = k.args
@@ -264,8 +320,7 @@ class WeightGradPlan(_Bound):
         self.status = None
         if self.n:
             need = dion_weight_grad_workspace(arr, self.n)
-            self._ws, self._ws_bytes = self._workspace(workspace, need)
-            self.status = torch.zeros(self.n, dtype=torch.int32, device=self._device)
+            self._ws, self._ws_bytes, self.status = self._workspace(workspace, need, self.n)
 
     def backward(self, accumulate=False, stream=None):
         if not self.n:
@@ -295,8 +350,8 @@ class SavedStep(_Bound):
                     raise ValueError(f"matrix {i}: its gradient is not {(s.m, s.n)}")
                 i += 1
         need = dion_step_from_saved_workspace(opt._h, self._arr, opt.num_matrices)
-        self._ws, self._ws_bytes = self._workspace(workspace, need)
-        self.grad_status = torch.zeros(opt.num_matrices, dtype=torch.int32, device=self._device)
+        self._ws, self._ws_bytes, self.grad_status = self._workspace(workspace, need,
+                                                                     opt.num_matrices)
 
     def step(self, X, M, G, Q, lr: float, status=None, accumulate=False, stream=None):
         arr = self.opt._ptrs(X, M, G, Q)
@@ -338,8 +393,7 @@ class NormPlan(_Bound):
         for name, t in (("pre_gain", pre_gain), ("post_gain", post_gain), ("gate", gate)):
             setattr(a, name, self._vector(name, t, x.shape[1]))
         if checkpoint is not None:
-            self._tensor("checkpoint", checkpoint.q)
-            self._keep.append(checkpoint)
+            self._checkpoint(checkpoint)
             a.kept = ctypes.pointer(checkpoint.args)
         self._args = a
         self._ref = ctypes.byref(a)
@@ -371,7 +425,7 @@ class NormGradPlan(_Bound):
                         ("dpre_gain", dpre_gain), ("dpost_gain", dpost_gain), ("dgate", dgate)):
             setattr(a, name, self._vector(name, t, h.shape[1]))
         need = dion_norm_backward_workspace(h.shape[0], h.shape[1])
-        self._ws, self._ws_bytes = self._workspace(workspace, need)
+        self._ws, self._ws_bytes, _ = self._workspace(workspace, need)
         self._args = a
         self._ref = ctypes.byref(a)
 
@@ -427,7 +481,7 @@ class EmbedGradPlan(_Bound):
         a.dtype = _dtype(dout)
         a.dtable, a.ldt = self._rows("dtable", dtable, dtable.shape, torch.float32)
         need = dion_embed_backward_workspace(ids.numel(), dtable.shape[1])
-        self._ws, self._ws_bytes = self._workspace(workspace, need)
+        self._ws, self._ws_bytes, _ = self._workspace(workspace, need)
         self._args = a
         self._ref = ctypes.byref(a)
 
