@@ -359,13 +359,12 @@ __global__ void __launch_bounds__(NT, 1)
       }
       if (!ok) break;
     }
-    if (*abort) {
-      // let every load already issued land before the CTA goes away
-      for (int i = 0; i < used; ++i) {
-        stage = (stage + p.stages - 1) % p.stages;
-        if (stage == p.stages - 1) phase ^= 1;
-        wait_drain(full + stage, phase);
-      }
+    // every load issued lands before the CTA goes away, whichever role gives up (and when: a
+    // role may do so after this one has issued its last load)
+    for (int i = 0; i < used; ++i) {
+      stage = (stage + p.stages - 1) % p.stages;
+      if (stage == p.stages - 1) phase ^= 1;
+      wait_drain(full + stage, phase);
     }
   } else if (warp == 1 && lane == 0) {
     // ---------------- MMA issuer
@@ -455,7 +454,9 @@ __global__ void __launch_bounds__(NT, 1)
       for (int ch = 0; ch < nch; ++ch) {
         const int acc = lt & 1;
         const uint32_t acc_phase = (lt >> 1) & 1;
-        if (!wait_bounded(tfull + acc, acc_phase, p.max_spins, abort)) { ok = false; break; }
+        // warp-uniform outcome: TMEM is read by whole warps
+        const bool w = wait_bounded(tfull + acc, acc_phase, p.max_spins, abort);
+        if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
         tc_fence_after();
         const int epi = (ch == 0 || tsum) ? p.epi : 2;
         const float alpha = p.epi == 0 ? 1.f : p.alpha;
@@ -1092,12 +1093,11 @@ __global__ void __launch_bounds__(FB_NT, 1)
       }
       if (!ok) break;
     }
-    if (*abort)
-      for (int i = 0; i < used; ++i) {
-        stage = (stage + FB_STAGES - 1) % FB_STAGES;
-        if (stage == FB_STAGES - 1) phase ^= 1;
-        wait_drain(f_full + stage, phase);
-      }
+    for (int i = 0; i < used; ++i) {  // as in k_tc_gemm
+      stage = (stage + FB_STAGES - 1) % FB_STAGES;
+      if (stage == FB_STAGES - 1) phase ^= 1;
+      wait_drain(f_full + stage, phase);
+    }
   } else if (warp == 3 && lane == 0) {
     // ---------------- TMA producer of the Q^T tiles
     prefetch_map(&tmQ);
@@ -1116,12 +1116,11 @@ __global__ void __launch_bounds__(FB_NT, 1)
       }
       if (!ok) break;
     }
-    if (*abort)
-      for (int i = 0; i < used; ++i) {
-        stage = (stage + FB_STAGES - 1) % FB_STAGES;
-        if (stage == FB_STAGES - 1) phase ^= 1;
-        wait_drain(b_full + stage, phase);
-      }
+    for (int i = 0; i < used; ++i) {  // as in k_tc_gemm
+      stage = (stage + FB_STAGES - 1) % FB_STAGES;
+      if (stage == FB_STAGES - 1) phase ^= 1;
+      wait_drain(b_full + stage, phase);
+    }
   } else if (warp == 1 && lane == 0) {
     // ---------------- MMA issuer
     int stage = 0, lt = 0;
@@ -1434,12 +1433,11 @@ __global__ void __launch_bounds__(NT, 1)
       }
       if (!ok) break;
     }
-    if (*abort)
-      for (int i = 0; i < used; ++i) {
-        stage = (stage + UPD_STAGES - 1) % UPD_STAGES;
-        if (stage == UPD_STAGES - 1) phase ^= 1;
-        wait_drain(full + stage, phase);
-      }
+    for (int i = 0; i < used; ++i) {  // as in k_tc_gemm
+      stage = (stage + UPD_STAGES - 1) % UPD_STAGES;
+      if (stage == UPD_STAGES - 1) phase ^= 1;
+      wait_drain(full + stage, phase);
+    }
   } else if (warp == 2 && lane == 0) {
     // ---------------- slab producer: M, G, X in 128 x 32 fp32 slabs
     prefetch_map(&tmM);
@@ -1471,12 +1469,11 @@ __global__ void __launch_bounds__(NT, 1)
       }
       if (!ok) break;
     }
-    if (*abort)
-      for (int i = 0; i < used; ++i) {
-        stage = (stage + SLAB_STAGES - 1) % SLAB_STAGES;
-        if (stage == SLAB_STAGES - 1) phase ^= 1;
-        wait_drain(sfull + stage, phase);
-      }
+    for (int i = 0; i < used; ++i) {  // as in k_tc_gemm
+      stage = (stage + SLAB_STAGES - 1) % SLAB_STAGES;
+      if (stage == SLAB_STAGES - 1) phase ^= 1;
+      wait_drain(sfull + stage, phase);
+    }
   } else if (warp == 1 && lane == 0) {
     // ---------------- MMA issuer: acc = P [R | Q]^T, M = 128, N = 256
     constexpr uint32_t idesc = idesc_bf16(BM, 2 * UPD_BN, false, false);
@@ -1520,14 +1517,17 @@ __global__ void __launch_bounds__(NT, 1)
     int lt = 0;
     bool ok = true;
     for (;; ++lt) {
-      if (!wait_bounded(ring_full + slot, rphase, p.max_spins, abort)) { ok = false; break; }
+      // warp-uniform outcomes, here and below: TMEM is read by whole warps
+      const bool rw = wait_bounded(ring_full + slot, rphase, p.max_spins, abort);
+      if (!__all_sync(0xffffffffu, rw)) { ok = false; break; }
       const int t = ring[slot];
       __syncwarp();
       if (lane == 0) mbar_arrive(ring_empty + slot);
       if (++slot == TILE_RING) { slot = 0; rphase ^= 1; }
       if (t < 0) break;
       const int acc = lt & 1;
-      if (!wait_bounded(tfull + acc, (lt >> 1) & 1, p.max_spins, abort)) { ok = false; break; }
+      const bool tw = wait_bounded(tfull + acc, (lt >> 1) & 1, p.max_spins, abort);
+      if (!__all_sync(0xffffffffu, tw)) { ok = false; break; }
       tc_fence_after();
       const int b = t / tiles_per_mat;
       const int rem = t % tiles_per_mat;
@@ -1542,7 +1542,8 @@ __global__ void __launch_bounds__(NT, 1)
         tmem_ld32(tbase + sl * SLAB, ar);
         tmem_ld32(tbase + UPD_BN + sl * SLAB, aq);
         tmem_wait_ld();
-        if (!wait_bounded(sfull + stage, phase, p.max_spins, abort)) { ok = false; break; }
+        const bool sw = wait_bounded(sfull + stage, phase, p.max_spins, abort);
+        if (!__all_sync(0xffffffffu, sw)) { ok = false; break; }
         uint8_t* slab = sS + stage * 3 * SLAB_BYTES;
         const uint8_t* rm = slab + row * 128;
         const uint8_t* rg = slab + SLAB_BYTES + row * 128;

@@ -69,3 +69,20 @@ def test_bounded_waits_time_out_cleanly():
     ref.step(1)
     assert _rel(ok.M[0], ref.M[0]) < 1e-5
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("shape,precision", [((4, 128, 128, 16), "bf16"), ((3, 512, 256, 64), "bf16"),
+                                             ((40, 256, 64, 64), "bf16"), ((2, 256, 384, 64), "fp32")])
+def test_give_up_over_short_products(shape, precision):
+    """The same with products of a few K blocks, whose producers have issued every load before
+    another role gives up: the loads land before their CTA ends, and the steps after are correct."""
+    wl = W.custom("timeout", [shape], precision=precision, steps=1)
+    ref = GpuRun(wl, kernel_path="simt")
+    ref.step(1)
+    for _ in range(3):
+        GpuRun(wl, kernel_path="tensor", max_wait_spins=1).step(1)
+        ok = GpuRun(wl, kernel_path="tensor")
+        ok.step(1)
+        assert not np.any(ok.status.cpu().numpy() & 8)
+        # as test_tensor_views_match_simt
+        assert _rel(ok.M[0], ref.M[0]) < 2e-4
