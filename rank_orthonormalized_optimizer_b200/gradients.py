@@ -143,6 +143,7 @@ class _Bound:
 
     def __init__(self):
         self._device, self._keep, self._owned = None, [], []
+        self._known = None      # the last call's stream, which may use all of _owned
 
     def _tensor(self, name, t, dtype=None):
         import torch
@@ -213,10 +214,17 @@ class _Bound:
                              f"cuda:{device}")
         # the handle alone: a Stream object takes longer than the launch
         raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+        if raw != self._known:
+            self._other_stream(raw, torch.cuda.current_stream(device) if stream is None else stream)
+        return raw
+
+    def _other_stream(self, raw, stream):
+        """The stream (another one than the last call's) may use the plan's own memory."""
         for owned in self._owned:
             if raw not in owned.streams:
-                owned.use(torch.cuda.current_stream(device) if stream is None else stream)
-        return raw
+                owned.use(stream)
+        if all(raw in owned.streams for owned in self._owned):
+            self._known = raw
 
 
 # ------------------------------------------------------------------ activations in 8 bits
