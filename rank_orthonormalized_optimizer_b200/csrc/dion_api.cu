@@ -818,7 +818,7 @@ dion_status dion_default_options(dion_options* opt) {
   opt->fallback_cond = 1e3f;
   opt->orth_tol = 2e-5f;
   opt->kernel_path = DION_PATH_TENSOR;
-  opt->max_wait_spins = int64_t(1) << 26;
+  opt->max_wait_spins = dion::kDefaultWaitSpins;
   opt->rmmc_threshold = 0.f;
   opt->stack_orth = 0;
   return DION_OK;
@@ -1265,8 +1265,8 @@ static dion_status dion_step_batched_from_saved_impl(dion_handle h, const dion_b
   if ((st = saved_sources(h, ptrs, sources, &list)) != DION_OK) return st;
   // every source is checked before the first gradient is enqueued; the workspace serves the
   // gradients first and then the step, in the order of the stream
-  st = dion_weight_grad(list.data(), (int32_t)list.size(), accumulate, d_workspace, workspace_bytes,
-                        grad_status, stream);
+  st = dion::weight_grad(list.data(), (int32_t)list.size(), accumulate, d_workspace, workspace_bytes,
+                         grad_status, h->opt.max_wait_spins, stream);
   if (st != DION_OK) return st;
   return dion_step_batched_impl(h, ptrs, nbuckets, lr, d_workspace, workspace_bytes, d_status, stream);
 }

@@ -12,6 +12,13 @@ namespace dion {
 
 // Record a message for dion_last_error() on this thread and return `s`.
 dion_status set_error(dion_status s, const char* fmt, ...);
+// Default of dion_options.max_wait_spins, and the limit of the calls without a handle.
+constexpr int64_t kDefaultWaitSpins = int64_t(1) << 26;
+
+// dion_weight_grad with a limit of its own on the device's waits (k_wgrad.cu).
+dion_status weight_grad(const dion_grad_source* src, int32_t nsrc, int32_t accumulate, void* ws,
+                        size_t ws_bytes, int32_t* d_status, int64_t max_spins, void* stream);
+
 // Workspace size of a valid handle's plan.
 dion_status plan_workspace_bytes(dion_handle h, size_t* bytes);
 

@@ -64,7 +64,6 @@ static_assert(SQ % kGroups == 0 && SA >= kGroups && SB >= SA, "a slot's previous
 constexpr int kItems = BK * BM / 16 / (32 * kGroupWarps);  // 16-feature groups per thread
 constexpr int Q_BYTES = BK * BM;
 constexpr int A_BYTES = BK * BM * 2;
-constexpr int64_t kMaxSpins = int64_t(1) << 26;
 
 struct WgradP {
   const uint8_t* scale;
@@ -171,6 +170,22 @@ __device__ __forceinline__ void tmem_alloc_pair(uint32_t* slot, uint32_t ncols) 
 }
 __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+// The last `stages` of the `issued` loads into a ring have landed.
+__device__ __forceinline__ void wait_landed(uint64_t* full, int stages, int issued) {
+  for (int j = max(0, issued - stages); j < issued; ++j) wait_drain(full + j % stages, (uint32_t)(j / stages) & 1);
+}
+// After a give-up, once every role of this CTA has stopped: the same for the 8-bit ring, whose
+// barriers also wait for the scale warp.  Either of the two may have gone further than the other;
+// the arrivals that are missing are made here, where nobody reads the tiles any more.
+__device__ __forceinline__ void land_scaled(uint64_t* full, int stages, int tiles, int scales) {
+  const int most = max(tiles, scales);
+  for (int j = max(0, most - stages); j < most; ++j) {
+    if (j >= tiles) mbar_arrive(full + j % stages);
+    for (int k = 0; k < 32 && j >= scales; ++k) mbar_arrive(full + j % stages);
+  }
+  wait_landed(full, stages, most);
 }
 
 // Four e4m3 bytes to bf16 times `f`: bytes 0 and 2 to `even`, 1 and 3 to `odd`.  A byte's 7
@@ -313,7 +328,7 @@ template <int BN> struct Smem {
   static constexpr int rings = SA * A_BYTES + SB * BK * BN + SQ * (Q_BYTES + 2 * BK * 4);
   static constexpr int epilogue = rings + 512;  // the barriers in between
   static constexpr int bytes = 1024 + epilogue + 8 * 32 * 9 * 4;
-  static_assert((2 * SQ + 2 * SB + 2 * SA + 5) * 8 + 16 <= 512, "the barriers");
+  static_assert((2 * SQ + 2 * SB + 2 * SA + 5) * 8 + 24 <= 512, "the barriers");
   static_assert(bytes <= 227 * 1024, "shared memory");
 };
 
@@ -340,7 +355,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-
+  volatile int* issued = abort + 1;        // stages of the 8-bit ring: tiles, scales
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -386,12 +401,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
       uint64_t *fullb = q ? q_full : b_full, *emptyb = q ? q_empty : b_empty;
       const int stages = q ? SQ : SB;
       prefetch_map(map);
-      int stage = 0, used = 0;
+      int stage = 0, count = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int u = pair; u < units && ok; u += pairs) {
         const Unit t = unit_of<BN>(p, u);
-        for (int kb = t.kb0; kb < t.kb1; ++kb) {
+        for (int kb = t.kb0; kb < t.kb1; ++kb, ++count) {
           if (!wait_bounded(emptyb + stage, phase ^ 1, p.max_spins, abort)) { ok = false; break; }
           mbar_expect_tx(fullb + stage, q ? Q_BYTES : B_BYTES);
           if (q) {
@@ -402,16 +417,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
               tma_load_2d(sB + stage * B_BYTES + j * 8192, map, fullb + stage,
                           t.n0 + rank * HB + 64 * j, kb * BK);
           }
-          if (used < stages) ++used;
           if (++stage == stages) { stage = 0; phase ^= 1; }
         }
       }
-      if (*abort)  // let every load already issued land before the CTA goes away
-        for (int i = 0; i < used; ++i) {
-          stage = (stage + stages - 1) % stages;
-          if (stage == stages - 1) phase ^= 1;
-          wait_drain(fullb + stage, phase);
-        }
+      // every load issued lands before the CTA goes away, whichever role gives up
+      if (q) issued[0] = count;
+      else wait_landed(fullb, stages, count);
     } else if (warp == 1 && lane == 0 && rank == 0) {
       // ---------------- MMA issuer of the pair: a stage is ready once the converters of both
       // CTAs, who waited for its D tile too, have arrived
@@ -444,15 +455,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
           if (acc == 0) pacc ^= 1;
         }
       }
-      asm volatile(
-          "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(drain))
-          : "memory");
+      commit_pair(drain);
       wait_drain(drain, 0);
     } else if (warp == 3) {
       // ---------------- scale bytes: the word of a token's four, or the two words that they
       // lie in, two tokens a lane
       const uintptr_t begin = reinterpret_cast<uintptr_t>(p.scale), end = begin + p.tokens * p.ld_scale;
-      int stage = 0;
+      int stage = 0, count = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int u = pair; u < units && ok; u += pairs) {
@@ -488,9 +497,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
           __threadfence_block();
           asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(q_full + stage))
                        : "memory");
+          ++count;
           if (++stage == SQ) { stage = 0; phase ^= 1; }
         }
       }
+      if (lane == 0) issued[1] = count;
       asm volatile("cp.async.wait_all;" ::: "memory");  // nothing in flight when the CTA ends
     }
   } else if (warp < 4 + kGroups * kGroupWarps) {
@@ -582,6 +593,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0) {  // every role of this CTA has stopped
+    if (*abort) land_scaled(q_full, SQ, issued[0], issued[1]);
+    if (rank != 0) wait_drain(drain, 0);  // the issuer's arrivals here have come
+  }
+  __syncwarp();
   cluster_sync();  // neither CTA leaves while the other may still reach its memory
   if (warp == 2) {
     tc_fence_after();
@@ -647,12 +663,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RNT, 1)
   if (warp == 0 && lane == 0) {
     prefetch_map(&tmA);
     prefetch_map(&tmD);
-    int stage = 0, used = 0;
+    int stage = 0, count = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (int u = pair; u < units && ok; u += pairs) {
       const Unit t = unit_of<RBN>(p, u);
-      for (int kb = t.kb0; kb < t.kb1; ++kb) {
+      for (int kb = t.kb0; kb < t.kb1; ++kb, ++count) {
         if (!wait_bounded(empty + stage, phase ^ 1, p.max_spins, abort)) { ok = false; break; }
         mbar_expect_tx(full + stage, R_STAGE);
         uint8_t* to = smem + stage * R_STAGE;
@@ -661,16 +677,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RNT, 1)
           tma_load_2d(to + j * 8192, &tmA, full + stage, t.m0 + rank * BM + 64 * j, kb * BK);
           tma_load_2d(to + A_BYTES + j * 8192, &tmD, full + stage, t.n0 + rank * (RBN / 2) + 64 * j, kb * BK);
         }
-        if (used < RS) ++used;
         if (++stage == RS) { stage = 0; phase ^= 1; }
       }
     }
-    if (*abort)  // let every load already issued land before the CTA goes away
-      for (int i = 0; i < used; ++i) {
-        stage = (stage + RS - 1) % RS;
-        if (stage == RS - 1) phase ^= 1;
-        wait_drain(full + stage, phase);
-      }
+    wait_landed(full, RS, count);  // whichever role gives up
   } else if (warp == 1 && lane == 0 && rank == 0) {
     constexpr uint32_t idesc = idesc_bf16(PM, RBN, true, true);
     int stage = 0, acc = 0;
@@ -699,9 +709,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RNT, 1)
         if (acc == 0) pacc ^= 1;
       }
     }
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(drain))
-        : "memory");
+    commit_pair(drain);
     wait_drain(drain, 0);
   } else if (warp == 3 && lane == 0) {
     int stage = 0;
@@ -721,6 +729,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RNT, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && rank != 0) wait_drain(drain, 0);  // as in k_wgrad
+  __syncwarp();
   cluster_sync();  // neither CTA leaves while the other may still reach its memory
   if (warp == 2) {
     tc_fence_after();
@@ -914,8 +924,8 @@ dion_status launch(WgradKernel kernel, int threads, int smem, const CUtensorMap&
   return launch_status("k_wgrad");
 }
 
-dion_status one_grad(const dion_grad_source& src, int accumulate, char* ws, int32_t* status, int sms,
-                     cudaStream_t s) {
+dion_status one_grad(const dion_grad_source& src, int accumulate, char* ws, int32_t* status,
+                     int64_t max_spins, int sms, cudaStream_t s) {
   const int64_t m = src.kept.features, n = src.n, tokens = src.kept.tokens;
   if (tokens == 0) {
     if (accumulate) return DION_OK;
@@ -969,7 +979,7 @@ dion_status one_grad(const dion_grad_source& src, int accumulate, char* ws, int3
   p.accumulate = accumulate != 0;
   p.vec = aligned_to(src.G, 32) && src.ldg % 8 == 0;
   p.scale4 = p.ld_scale % 4 == 0 && aligned_to(p.scale, 4);
-  p.max_spins = kMaxSpins;
+  p.max_spins = max_spins;
   const dion_status st = g.rows        ? launch(k_wgrad_rows, RNT, kRowsSmem, mq, md, p, sms, s)
                          : g.bn == 256 ? launch(k_wgrad<256>, NT, Smem<256>::bytes, mq, md, p, sms, s)
                                        : launch(k_wgrad<128>, NT, Smem<128>::bytes, mq, md, p, sms, s);
@@ -978,8 +988,10 @@ dion_status one_grad(const dion_grad_source& src, int accumulate, char* ws, int3
                                                     1024, 0, s, p, g.bn));
 }
 
-dion_status wgrad_impl(const dion_grad_source* src, int32_t nsrc, int32_t accumulate, void* ws,
-                       size_t ws_bytes, int32_t* d_status, void* stream) {
+}  // namespace
+
+dion_status weight_grad(const dion_grad_source* src, int32_t nsrc, int32_t accumulate, void* ws,
+                        size_t ws_bytes, int32_t* d_status, int64_t max_spins, void* stream) {
   if (nsrc < 0) return set_error(DION_ERR_INVALID_ARG, "nsources < 0");
   if (nsrc > 0 && !src) return set_error(DION_ERR_INVALID_ARG, "sources is NULL");
   for (int32_t i = 0; i < nsrc; ++i) DION_TRY(check_source(src[i], i));
@@ -993,12 +1005,11 @@ dion_status wgrad_impl(const dion_grad_source* src, int32_t nsrc, int32_t accumu
   int sms = 0;
   DION_TRY(check_sm100(&sms));
   for (int32_t i = 0; i < nsrc; ++i)
-    DION_TRY(one_grad(src[i], accumulate, static_cast<char*>(ws), d_status ? d_status + i : nullptr, sms,
-                      reinterpret_cast<cudaStream_t>(stream)));
+    DION_TRY(one_grad(src[i], accumulate, static_cast<char*>(ws), d_status ? d_status + i : nullptr,
+                      max_spins, sms, reinterpret_cast<cudaStream_t>(stream)));
   return DION_OK;
 }
 
-}  // namespace
 }  // namespace dion
 
 extern "C" {
@@ -1017,7 +1028,8 @@ size_t dion_weight_grad_workspace(const dion_grad_source* sources, int32_t nsour
 dion_status dion_weight_grad(const dion_grad_source* sources, int32_t nsources, int32_t accumulate,
                              void* d_workspace, size_t workspace_bytes, int32_t* d_status,
                              void* stream) {
-  return dion::wgrad_impl(sources, nsources, accumulate, d_workspace, workspace_bytes, d_status, stream);
+  return dion::weight_grad(sources, nsources, accumulate, d_workspace, workspace_bytes, d_status,
+                           dion::kDefaultWaitSpins, stream);
 }
 
 }  // extern "C"
