@@ -71,7 +71,9 @@ enum {
   DION_MAT_CHOLQR2 = 2,       /* a second Cholesky-QR pass was applied                   */
   DION_MAT_NONFINITE = 4,     /* a Gram matrix held Inf/NaN (inputs were not finite)     */
   DION_MAT_TIMEOUT = 8,       /* a bounded device wait ran out; this matrix's outputs
-                                 are not valid and X, M, Q may be partly updated         */
+                                 are not valid and X, M, Q may be partly updated (where it
+                                 was its gradient's in dion_step_batched_from_saved: they
+                                 are as they were)                                       */
   DION_MAT_ZERO_COLUMN = 16,  /* some column of R had zero norm; its Q column is zero    */
   DION_MAT_HIGH_RMMC = 32     /* the momentum changed faster than rmmc_threshold: RMMC =
                                  max|M' - M| / max|M| > rmmc_threshold (CurvaDion's gate:
@@ -125,8 +127,9 @@ typedef struct dion_options {
   float fallback_cond;     /* Householder when max L_kk / min L_kk exceeds it (1e3)        */
   float orth_tol;          /* AUTO: second pass when max|P^T P - I| > orth_tol (2e-5)      */
   int32_t kernel_path;     /* dion_kernel_path (default DION_PATH_TENSOR)                  */
-  int64_t max_wait_spins;  /* bound on every device-side wait; when it runs out the
-                              kernel sets DION_MAT_TIMEOUT and returns (default 1<<26)     */
+  int64_t max_wait_spins;  /* bound on every device-side wait of the handle's calls; when
+                              it runs out the kernel sets DION_MAT_TIMEOUT and returns
+                              (default 1<<26, which dion_weight_grad has, too)             */
   float rmmc_threshold;    /* DION_MAT_HIGH_RMMC where RMMC exceeds it (default 0: every
                               matrix whose momentum moved; not NaN)                        */
   int32_t stack_orth;      /* 1: buckets of equal m and r share one orthonormalisation
@@ -507,7 +510,8 @@ size_t dion_weight_grad_workspace(const dion_grad_source* sources, int32_t nsour
 
 /* Every gradient of the list, one after the other.  d_status (may be NULL): device int32,
  * one word per source, into which DION_MAT_TIMEOUT is OR-ed where a bounded device wait
- * ran out (that gradient is then not valid). */
+ * ran out (that gradient is then not valid: parts of it were not written, or not added).  It
+ * is not cleared. */
 dion_status dion_weight_grad(const dion_grad_source* sources, int32_t nsources, int32_t accumulate,
                              void* d_workspace, size_t workspace_bytes, int32_t* d_status,
                              void* stream);
@@ -518,7 +522,9 @@ dion_status dion_weight_grad(const dion_grad_source* sources, int32_t nsources, 
  * slot of ptrs[b].G (which this call therefore overwrites; the sources' own G and ldg are
  * not read).  Each source must have the matrix's shape: features x n, or n x features where
  * transposed.  `accumulate` != 0 adds to what ptrs[b].G holds (the earlier micro-batches).
- * grad_status (may be NULL) is dion_weight_grad's d_status.  The workspace must have
+ * grad_status (may be NULL) is dion_weight_grad's d_status.  Where a wait of a gradient ran out
+ * in this call, the step leaves that matrix's X, M and Q as they are and reports
+ * DION_MAT_TIMEOUT in d_status, too.  The workspace must have
  * dion_step_from_saved_workspace bytes.
  */
 size_t dion_step_from_saved_workspace(dion_handle h, const dion_grad_source* sources,

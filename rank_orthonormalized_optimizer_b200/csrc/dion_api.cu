@@ -177,6 +177,7 @@ struct StepCtx {
   std::vector<int> p0s_ready;  // per bucket: P0's split was written by B Q
   bool sharded = false;        // R is a partial sum: column-norm partials from R itself
   std::vector<int> g_ready;    // per stack: P0's split was written by every member's B Q
+  const int32_t* held = nullptr;  // per matrix: not zero where its gradient is not valid
 };
 
 void begin_cls(StepCtx& c, int cls) {
@@ -391,6 +392,7 @@ dion_status run_bucket(StepCtx& c, int bi, int phase, const Plan& p, const dion_
   __nv_bfloat16* Ws = p.off_Ws ? reinterpret_cast<__nv_bfloat16*>(ws + p.off_Ws) : nullptr;
   __nv_bfloat16* Ts = p.off_Ts ? reinterpret_cast<__nv_bfloat16*>(ws + p.off_Ts) : nullptr;
   // PH_ORTH runs once per stack (bi is then the stack's index and p its plan)
+  const int32_t* held = c.held ? c.held + p.mat0 : nullptr;
   int& p0s_ready = phase == PH_ORTH ? c.g_ready[bi] : c.p0s_ready[bi];
   const int64_t plane_mr = (int64_t)p.zplane * p.m * p.r;  // between split parts of m x r
   const int64_t m = p.m, n = p.n, r = p.r;
@@ -401,13 +403,13 @@ dion_status run_bucket(StepCtx& c, int bi, int phase, const Plan& p, const dion_
     p0s_ready = 0;
     DION_LAUNCH(c, 1, dion::launch_init_flags(flags, stats, sched, rmmc, cnt,
                                               o.orth_mode == DION_ORTH_HOUSEHOLDER ? DION_MAT_FALLBACK : 0,
-                                              s));
+                                              held, s));
     // a stack of several buckets has counters of its own (the fallback loop's rounds)
     const OrthGroup& g = c.h->groups[p.group];
     if (g.members.size() > 1 && g.members[0] == bi)
       DION_LAUNCH(c, 1, dion::launch_init_flags(nullptr, nullptr,
                                                 reinterpret_cast<int*>(ws + g.orth.off_sched),
-                                                nullptr, 0, 0, s));
+                                                nullptr, 0, 0, nullptr, s));
     return DION_OK;
   }
 
@@ -650,7 +652,7 @@ dion_status run_bucket(StepCtx& c, int bi, int phase, const Plan& p, const dion_
   begin_cls(c, DION_KCLASS_COLNORM);
   DION_LAUNCH(c, 2,
               dion::launch_colnorm(R, bp.Q, Rg, Qng, bf ? 1 : (split ? 2 : 0), part, p.nsplit,
-                                   tensor && !c.sharded, flags, cnt, n, r, s));
+                                   tensor && !c.sharded, flags, held, cnt, n, r, s));
   end_cls(c);
   return DION_OK;
   }
@@ -664,8 +666,8 @@ dion_status run_bucket(StepCtx& c, int bi, int phase, const Plan& p, const dion_
     if (tensor) {
       int nl = 0;
       cudaError_t e = dion::tc_update(Pg, p.zplane, Rg, Qng, split, bp.G, bp.M, bp.X, cnt, m, n,
-                                      r, o.mu, lrs, o.max_wait_spins, flags, sched, rmmc, s, &nl,
-                                      &done);
+                                      r, o.mu, lrs, o.max_wait_spins, flags, held, sched, rmmc, s,
+                                      &nl, &done);
       c.launches += nl;
       if (e != cudaSuccess) return fail(DION_ERR_CUDA, "tc_update: %s", cudaGetErrorString(e));
       if (!done) return fail(DION_ERR_CUDA, "tc_update: %s", dion::tc_map_error());
@@ -673,7 +675,7 @@ dion_status run_bucket(StepCtx& c, int bi, int phase, const Plan& p, const dion_
     if (!done)
       DION_LAUNCH(c, (cnt + 65534) / 65535,
                   dion::launch_update_simt(Pg, Rg, Qng, bf, bp.G, bp.M, bp.X, cnt, m, n, r, o.mu,
-                                           lrs, rmmc, s));
+                                           lrs, rmmc, held, s));
   }
   end_cls(c);
   return DION_OK;
@@ -1035,7 +1037,7 @@ static dion_status dion_init_impl(const dion_bucket_desc* buckets, const dion_sh
 
 static dion_status dion_step_batched_impl(dion_handle h, const dion_bucket_ptrs* ptrs, int32_t nbuckets,
                               float lr, void* d_workspace, size_t workspace_bytes,
-                              int32_t* d_status, void* stream) {
+                              int32_t* d_status, void* stream, const int32_t* held = nullptr) {
   dion_status st = check_step_args(h, ptrs, nbuckets, d_workspace, workspace_bytes, d_status);
   if (st != DION_OK) return st;
   if (h->sharded)
@@ -1043,6 +1045,7 @@ static dion_status dion_step_batched_impl(dion_handle h, const dion_bucket_ptrs*
   if (!std::isfinite(lr)) return fail(DION_ERR_INVALID_ARG, "lr is not finite");
   cudaStream_t main = reinterpret_cast<cudaStream_t>(stream);
   StepCtx c{h, main, 0, -1, nullptr, 0, std::vector<int>(nbuckets, 0)};
+  c.held = held;
   char* ws = static_cast<char*>(d_workspace);
   // Each stack's orthonormalisation is a chain of short, latency-bound kernels that
   // needs only its buckets' P0.  It is forked onto the stack's own stream as soon as the
@@ -1247,6 +1250,11 @@ static dion_status saved_sources(dion_handle h, const dion_bucket_ptrs* ptrs,
   return DION_OK;
 }
 
+// Workspace of the gradients and of the step, which take turns in it.
+static size_t saved_work_bytes(dion_handle h, const dion_grad_source* sources, int32_t nsources) {
+  return align_up(std::max(h->ws_bytes, dion_weight_grad_workspace(sources, nsources)), 256);
+}
+
 static dion_status dion_step_batched_from_saved_impl(dion_handle h, const dion_bucket_ptrs* ptrs,
                                                      const dion_grad_source* sources,
                                                      int32_t nbuckets, int32_t accumulate, float lr,
@@ -1259,16 +1267,31 @@ static dion_status dion_step_batched_from_saved_impl(dion_handle h, const dion_b
   if (!std::isfinite(lr)) return fail(DION_ERR_INVALID_ARG, "lr is not finite");
   std::vector<dion_grad_source> list;
   dion_status st = saved_sources(h, nullptr, sources, &list);  // the shapes
-  if (st == DION_OK) st = check_step_args(h, ptrs, nbuckets, d_workspace, workspace_bytes, d_status);
+  if (st != DION_OK) return st;
+  const size_t work = saved_work_bytes(h, list.data(), (int32_t)list.size());
+  const size_t words = list.size() * sizeof(int32_t);
+  if (d_workspace && workspace_bytes < work + words)
+    return fail(DION_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes, %zu needed", workspace_bytes,
+                work + words);
+  if (grad_status && (reinterpret_cast<uintptr_t>(grad_status) & 3u))
+    return fail(DION_ERR_MISALIGNED, "grad_status is not 4-byte aligned");
+  st = check_step_args(h, ptrs, nbuckets, d_workspace, workspace_bytes, d_status);
   if (st != DION_OK) return st;
   list.clear();
   if ((st = saved_sources(h, ptrs, sources, &list)) != DION_OK) return st;
   // every source is checked before the first gradient is enqueued; the workspace serves the
-  // gradients first and then the step, in the order of the stream
-  st = dion::weight_grad(list.data(), (int32_t)list.size(), accumulate, d_workspace, workspace_bytes,
-                         grad_status, h->opt.max_wait_spins, stream);
+  // gradients first and then the step, in the order of the stream, and its last words say which
+  // gradients ran out of waits: the step leaves those matrices alone
+  int32_t* held = reinterpret_cast<int32_t*>(static_cast<char*>(d_workspace) + work);
+  st = dion::weight_grad(list.data(), (int32_t)list.size(), accumulate, d_workspace, work, held, true,
+                         h->opt.max_wait_spins, stream);
   if (st != DION_OK) return st;
-  return dion_step_batched_impl(h, ptrs, nbuckets, lr, d_workspace, workspace_bytes, d_status, stream);
+  if (grad_status) {
+    const cudaError_t e = dion::launch_or_words(grad_status, held, (int64_t)list.size(),
+                                                reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(DION_ERR_CUDA, "k_or_words: %s", cudaGetErrorString(e));
+  }
+  return dion_step_batched_impl(h, ptrs, nbuckets, lr, d_workspace, work, d_status, stream, held);
 }
 
 // ------------------------------------------------------------ row-sharded step
@@ -1695,8 +1718,7 @@ size_t dion_step_from_saved_workspace(dion_handle h, const dion_grad_source* sou
   size_t bytes = 0;
   guarded("dion_step_from_saved_workspace", [&] {
     if (!valid(h)) return fail(DION_ERR_NOT_INITIALIZED, "invalid or freed handle");
-    bytes = dion_weight_grad_workspace(sources, nsources);
-    if (bytes < h->ws_bytes) bytes = h->ws_bytes;
+    bytes = saved_work_bytes(h, sources, nsources) + (size_t)std::max(nsources, 0) * sizeof(int32_t);
     return DION_OK;
   });
   return bytes;

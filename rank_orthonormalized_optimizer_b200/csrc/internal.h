@@ -15,9 +15,12 @@ dion_status set_error(dion_status s, const char* fmt, ...);
 // Default of dion_options.max_wait_spins, and the limit of the calls without a handle.
 constexpr int64_t kDefaultWaitSpins = int64_t(1) << 26;
 
-// dion_weight_grad with a limit of its own on the device's waits (k_wgrad.cu).
+// dion_weight_grad with a limit of its own on the device's waits; clear: d_status is zeroed
+// first, so that it speaks of this call alone (k_wgrad.cu).
 dion_status weight_grad(const dion_grad_source* src, int32_t nsrc, int32_t accumulate, void* ws,
-                        size_t ws_bytes, int32_t* d_status, int64_t max_spins, void* stream);
+                        size_t ws_bytes, int32_t* d_status, bool clear, int64_t max_spins, void* stream);
+// dst[i] |= src[i]
+cudaError_t launch_or_words(int32_t* dst, const int32_t* src, int64_t n, cudaStream_t s);
 
 // Workspace size of a valid handle's plan.
 dion_status plan_workspace_bytes(dion_handle h, size_t* bytes);
@@ -53,9 +56,11 @@ cudaError_t launch_form_b_split(const float* M, const float* G, void* Bs, int64_
 cudaError_t launch_prep_q_split(const float* Q, void* Qs, int count, int64_t n, int64_t r,
                                 cudaStream_t s);
 // Zero the per-matrix flags (or set init_bits), the Cholesky statistics and the 16
-// tile counters of the bucket's dynamically scheduled kernels.
+// tile counters of the bucket's dynamically scheduled kernels.  held (may be null, here and
+// below): a word per matrix; where it is not zero the matrix's gradient is not valid, its flags
+// start as DION_MAT_TIMEOUT and its X, M and Q are left as they are.
 cudaError_t launch_init_flags(int32_t* flags, float* stats, int* sched, float* rmmc, int count,
-                              int32_t init_bits, cudaStream_t s);
+                              int32_t init_bits, const int32_t* held, cudaStream_t s);
 // mode 0: fp32 P only; 1: + bf16 copy Pg; 2: + three-way bf16 split Pg.  pg_ready: Pg
 // already holds the first pass's P; only second-pass and fallback matrices are written.
 cudaError_t launch_finalize_p(const float* P2, void* Pg, int mode, const int32_t* flags,
@@ -66,8 +71,8 @@ int colnorm_splits(int count, int64_t n);
 // partial column sums of squares per matrix ([count][nsplit][r]); part_ready: B^T P wrote
 // them already (else a first kernel does, over nsplit row ranges).
 cudaError_t launch_colnorm(const float* R, float* Q, void* Rg, void* Qg, int mode,
-                           float* part, int nsplit, bool part_ready, int32_t* flags, int count,
-                           int64_t n, int64_t r, cudaStream_t s);
+                           float* part, int nsplit, bool part_ready, int32_t* flags,
+                           const int32_t* held, int count, int64_t n, int64_t r, cudaStream_t s);
 cudaError_t launch_split3(const float* src, void* dst, int64_t n, int64_t dst_stride,
                           cudaStream_t s);
 // RMMC = max |M' - M| / max |M| per matrix (rmmc: [3][count], the third plane written;
@@ -97,7 +102,7 @@ cudaError_t launch_gemm_simt(const GemmDesc& d, bool bf16_operands, cudaStream_t
 cudaError_t launch_update_simt(const void* Pg, const void* Rg, const void* Qg, bool use_bf16,
                                const float* G, float* M, float* X, int count, int64_t m,
                                int64_t n, int64_t r, float mu, float lr_scale, float* rmmc,
-                               cudaStream_t s);
+                               const int32_t* held, cudaStream_t s);
 
 // ---- orthonormalisation (k_orth.cu)
 // pass 1: Cholesky of W = P0^T P0; pass 2: checks W = P1^T P1 first.

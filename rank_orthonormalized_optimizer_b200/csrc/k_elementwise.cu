@@ -201,11 +201,11 @@ cudaError_t launch_split3(const float* src, void* dst, int64_t n, int64_t dst_st
 
 // ---------------------------------------------------------- flags and status
 __global__ void k_init_flags(int32_t* flags, float* stats, int* sched, float* rmmc, int count,
-                             int32_t init_bits) {
+                             int32_t init_bits, const int32_t* held) {
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
   if (b < 16) sched[b] = 0;
   if (b < count) {
-    flags[b] = init_bits;
+    flags[b] = init_bits | (held && held[b] ? F_TIMEOUT : 0);
     stats[ST * b] = 3.0e38f;     // running min of diag(L)
     stats[ST * b + 1] = 0.f;     // running max of diag(L)
     stats[ST * b + 2] = 0.f;
@@ -216,9 +216,19 @@ __global__ void k_init_flags(int32_t* flags, float* stats, int* sched, float* rm
 }
 
 cudaError_t launch_init_flags(int32_t* flags, float* stats, int* sched, float* rmmc, int count,
-                              int32_t init_bits, cudaStream_t s) {
+                              int32_t init_bits, const int32_t* held, cudaStream_t s) {
   const int n = count > 16 ? count : 16;
-  k_init_flags<<<(n + 255) / 256, 256, 0, s>>>(flags, stats, sched, rmmc, count, init_bits);
+  k_init_flags<<<(n + 255) / 256, 256, 0, s>>>(flags, stats, sched, rmmc, count, init_bits, held);
+  return cudaGetLastError();
+}
+
+__global__ void k_or_words(int32_t* dst, const int32_t* src, int64_t n) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < n) dst[i] |= src[i];
+}
+
+cudaError_t launch_or_words(int32_t* dst, const int32_t* src, int64_t n, cudaStream_t s) {
+  k_or_words<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(dst, src, n);
   return cudaGetLastError();
 }
 
@@ -461,11 +471,13 @@ __global__ void __launch_bounds__(256) k_colnorm_apply(const float* __restrict__
                                                         void* __restrict__ Rg,
                                                         void* __restrict__ Qg,
                                                         const float* __restrict__ part,
-                                                        int32_t* __restrict__ flags, int64_t n,
+                                                        int32_t* __restrict__ flags,
+                                                        const int32_t* __restrict__ held, int64_t n,
                                                         int64_t r, int nsplit, int64_t part_bs,
                                                         int64_t rows_per_block) {
   extern __shared__ __align__(16) float norm_s[];  // r floats
   const int64_t b = blockIdx.y;
+  if (held && held[b]) return;  // nor does the update read its operands
   bool zero = false;
   for (int64_t j = threadIdx.x; j < r; j += blockDim.x) {
     float ss = 0.f;
@@ -537,8 +549,8 @@ int colnorm_splits(int count, int64_t n) {
 }
 
 cudaError_t launch_colnorm(const float* R, float* Q, void* Rg, void* Qg, int mode, float* part,
-                           int nsplit, bool part_ready, int32_t* flags, int count, int64_t n,
-                           int64_t r, cudaStream_t s) {
+                           int nsplit, bool part_ready, int32_t* flags, const int32_t* held,
+                           int count, int64_t n, int64_t r, cudaStream_t s) {
   const int64_t vc = r / 4;
   if (!part_ready) {
     const size_t red_bytes = (size_t)(vc >= 256 ? 256 : 256 / vc * vc) * sizeof(float4);
@@ -565,14 +577,14 @@ cudaError_t launch_colnorm(const float* R, float* Q, void* Rg, void* Qg, int mod
   }
   const dim3 grid((unsigned)gx, (unsigned)count);
   if (mode == 2)
-    k_colnorm_apply<2><<<grid, 256, smem, s>>>(R, Q, Rg, Qg, part, flags, n, r, nsplit, part_bs,
-                                               rows);
+    k_colnorm_apply<2><<<grid, 256, smem, s>>>(R, Q, Rg, Qg, part, flags, held, n, r, nsplit,
+                                               part_bs, rows);
   else if (mode == 1)
-    k_colnorm_apply<1><<<grid, 256, smem, s>>>(R, Q, Rg, Qg, part, flags, n, r, nsplit, part_bs,
-                                               rows);
+    k_colnorm_apply<1><<<grid, 256, smem, s>>>(R, Q, Rg, Qg, part, flags, held, n, r, nsplit,
+                                               part_bs, rows);
   else
-    k_colnorm_apply<0><<<grid, 256, smem, s>>>(R, Q, Rg, Qg, part, flags, n, r, nsplit, part_bs,
-                                               rows);
+    k_colnorm_apply<0><<<grid, 256, smem, s>>>(R, Q, Rg, Qg, part, flags, held, n, r, nsplit,
+                                               part_bs, rows);
   return cudaGetLastError();
 }
 

@@ -138,11 +138,13 @@ __global__ void __launch_bounds__(NT) k_update_simt(const T* __restrict__ Pg,
                                                      float* __restrict__ M, float* __restrict__ X,
                                                      int64_t m, int64_t n, int64_t r,
                                                      float one_minus_mu, float lr_scale,
-                                                     float* __restrict__ rmmc, int batch) {
+                                                     float* __restrict__ rmmc, int batch,
+                                                     const int32_t* __restrict__ held) {
   __shared__ __align__(16) float Ps[BK][BM + 4];
   __shared__ __align__(16) float Rs[BK][BN + 4];
   __shared__ __align__(16) float Qs[BK][BN + 4];
   const int64_t b = blockIdx.z;
+  if (held && held[b]) return;
   const int64_t i0 = (int64_t)blockIdx.y * BM, j0 = (int64_t)blockIdx.x * BN;
   const T* P = Pg + b * m * r;
   const T* R = Rg + b * n * r;
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(NT) k_update_simt(const T* __restrict__ Pg,
 cudaError_t launch_update_simt(const void* Pg, const void* Rg, const void* Qg, bool use_bf16,
                                const float* G, float* M, float* X, int count, int64_t m,
                                int64_t n, int64_t r, float mu, float lr_scale, float* rmmc,
-                               cudaStream_t s) {
+                               const int32_t* held, cudaStream_t s) {
   for (int b0 = 0; b0 < count; b0 += 65535) {
     const int nb = (count - b0) < 65535 ? (count - b0) : 65535;
     dim3 grid((unsigned)((n + BN - 1) / BN), (unsigned)((m + BM - 1) / BM), (unsigned)nb);
@@ -233,12 +235,12 @@ cudaError_t launch_update_simt(const void* Pg, const void* Rg, const void* Qg, b
       k_update_simt<bf16><<<grid, NT, 0, s>>>(
           (const bf16*)Pg + (size_t)b0 * m * r, (const bf16*)Rg + (size_t)b0 * n * r,
           (const bf16*)Qg + (size_t)b0 * n * r, G + mn, M + mn, X + mn, m, n, r, 1.f - mu,
-          lr_scale, rmmc + b0, count);
+          lr_scale, rmmc + b0, count, held ? held + b0 : nullptr);
     else
       k_update_simt<float><<<grid, NT, 0, s>>>(
           (const float*)Pg + (size_t)b0 * m * r, (const float*)Rg + (size_t)b0 * n * r,
           (const float*)Qg + (size_t)b0 * n * r, G + mn, M + mn, X + mn, m, n, r, 1.f - mu,
-          lr_scale, rmmc + b0, count);
+          lr_scale, rmmc + b0, count, held ? held + b0 : nullptr);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }

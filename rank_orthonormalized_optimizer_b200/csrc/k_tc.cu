@@ -1320,6 +1320,7 @@ struct UpdP {
   int zplane_p;       // matrices between P's split parts
   int64_t max_spins;
   float* rmmc;        // [2][batch]: max |M' - M| and max |M| per matrix (max-ed into)
+  const int32_t* held;  // matrices that are not updated (may be null)
 };
 
 // Tiles are handed out in order from a global counter rather than dealt round-robin:
@@ -1409,6 +1410,7 @@ __global__ void __launch_bounds__(NT, 1)
       if (!wait_bounded(ring_empty + slot, rphase ^ 1, p.max_spins, abort)) break;
       int t = atomicAdd(p.tile_counter, 1);
       if (t >= ntiles) t = -1;
+      else if (p.held && p.held[t / tiles_per_mat]) continue;
       ring[slot] = t;
       mbar_arrive(ring_full + slot);  // publishes the tile id to the consumers
       if (++slot == TILE_RING) { slot = 0; rphase ^= 1; }
@@ -1617,7 +1619,8 @@ __global__ void __launch_bounds__(NT, 1)
 cudaError_t tc_update(const void* Pg, int zplane_p, const void* Rg, const void* Qg, bool split,
                       const float* G, float* M, float* X, int count, int64_t m, int64_t n,
                       int64_t r, float mu, float lr_scale, int64_t max_spins, int32_t* flags,
-                      int* tile_counter, float* rmmc, cudaStream_t s, int* nlaunch, bool* done) {
+                      const int32_t* held, int* tile_counter, float* rmmc, cudaStream_t s,
+                      int* nlaunch, bool* done) {
   using namespace tc;
   *nlaunch = 0;
   *done = false;
@@ -1649,6 +1652,7 @@ cudaError_t tc_update(const void* Pg, int zplane_p, const void* Rg, const void* 
   p.zplane_p = zp;
   p.max_spins = max_spins;
   p.rmmc = rmmc;
+  p.held = held;
   cudaError_t e = cudaFuncSetAttribute(k_tc_update, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)UPD_SMEM);
   if (e != cudaSuccess) return e;

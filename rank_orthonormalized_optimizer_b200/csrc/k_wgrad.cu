@@ -31,7 +31,9 @@
 // 1227 us for m = 4096, n = 11008; chunks of 8 blocks 1.3e-7 at 1258 us, of 4 8e-8 at 1319 us.
 // The tiles that do not fill a last round over all pairs (all of them, in a small matrix) are
 // also split over the tokens, so that every pair has a share; their partial sums go to the
-// workspace and a second kernel adds them in order.  Every wait is bounded.
+// workspace and a second kernel adds them in order.  Every wait is bounded; after a give-up the
+// CTA lets its loads and MMAs end, marks DION_MAT_TIMEOUT and leaves what it has not finished of G
+// as it was.
 #include <cuda.h>
 
 #include <algorithm>
@@ -69,11 +71,13 @@ struct WgradP {
   const uint8_t* scale;
   float* out;        // G
   float* parts;      // [tail tile][split][PM][BN]: partial sums of the split tiles
+  int32_t* gave_up;  // [CTA]: whether a wait of it ran out in this call (null without a join)
   int32_t* status;
   int64_t tokens, ld_scale, ldg, m, n;
   int tiles_m, whole, tail;               // tiles taken whole, and split over the tokens
   int splits, blocks_per_split, blocks;   // blocks: of 64 tokens
   int transposed, accumulate, vec;
+  int ctas;          // of the kernel
   int scale4;        // the scale bytes of a tile's token are an aligned word
   int64_t max_spins;
 };
@@ -391,6 +395,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   const uint32_t tmem = *tmem_slot;
 
   grid_trigger();  // a grid of one round: the join's CTAs come as these end
+  // (by a thread without a role, so that nothing waits for the store)
+  if (threadIdx.x == 33 && p.gave_up) p.gave_up[blockIdx.x] = 0;
   if (warp < 4) {
     reg_dec<40>();
     if ((warp == 0 || warp == 2) && lane == 0) {
@@ -594,7 +600,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0) {  // every role of this CTA has stopped
-    if (*abort) land_scaled(q_full, SQ, issued[0], issued[1]);
+    if (*abort) {
+      if (p.gave_up) p.gave_up[blockIdx.x] = 1;
+      land_scaled(q_full, SQ, issued[0], issued[1]);
+    }
     if (rank != 0) wait_drain(drain, 0);  // the issuer's arrivals here have come
   }
   __syncwarp();
@@ -660,6 +669,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RNT, 1)
   const uint32_t tmem = *tmem_slot;
 
   grid_trigger();
+  if (threadIdx.x == 33 && p.gave_up) p.gave_up[blockIdx.x] = 0;  // as in k_wgrad
   if (warp == 0 && lane == 0) {
     prefetch_map(&tmA);
     prefetch_map(&tmD);
@@ -729,7 +739,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RNT, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0 && rank != 0) wait_drain(drain, 0);  // as in k_wgrad
+  if (threadIdx.x == 0) {  // as in k_wgrad (the rank read again: kept over the roles it would spill)
+    if (*abort && p.gave_up) p.gave_up[blockIdx.x] = 1;
+    if (cluster_rank() != 0) wait_drain(drain, 0);
+  }
   __syncwarp();
   cluster_sync();  // neither CTA leaves while the other may still reach its memory
   if (warp == 2) {
@@ -739,7 +752,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RNT, 1)
 }
 
 // Adds the split tiles' partial sums in order, into G in either layout: 32 x 32 of a tile, an
-// element a thread, so that a small matrix's few blocks have their loads in flight at once.
+// element a thread, so that a small matrix's few blocks have their loads in flight at once.  Where
+// a CTA gave up, parts may be missing: then G stays as it was.
 __global__ void __launch_bounds__(1024) k_wgrad_join(const WgradP p, int bn) {
   __shared__ float block[32][33];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
@@ -748,11 +762,13 @@ __global__ void __launch_bounds__(1024) k_wgrad_join(const WgradP p, int bn) {
   const int64_t row0 = (int64_t)(tile % p.tiles_m) * PM + i0, col0 = (int64_t)(tile / p.tiles_m) * bn + j0;
   if (row0 >= p.m || col0 >= p.n) return;
   grid_wait();
+  const int missing = threadIdx.x < p.ctas ? p.gave_up[threadIdx.x] : 0;
   const int64_t plane = (int64_t)PM * bn;
   const float* from = p.parts + blockIdx.z * p.splits * plane + (int64_t)(i0 + ty) * bn + j0 + tx;
   float sum = 0.f;
 #pragma unroll 8
   for (int s = 0; s < p.splits; ++s) sum += from[s * plane];
+  if (__syncthreads_or(missing)) return;
   int64_t i = row0 + ty, j = col0 + tx;
   if (!p.transposed) {
     if (i >= p.m || j >= p.n) return;
@@ -840,6 +856,7 @@ dion_status map2d(CUtensorMap* m, const void* base, CUtensorMapDataType type,
 // Pairs of SMs, and the fewest blocks in a split: below two, a pair's start and the join cost
 // more than the tokens.  Plans (and so workspace sizes) do not depend on the device asked.
 constexpr int kPairs = 74, kMinBlocks = 2;
+constexpr int kMaxCtas = 1024;  // of a launch: k_wgrad_join looks at each with a thread
 // What a block of 64 tokens costs a pair, and what parts and their join cost: a launch, and a share
 // for each tile and each part, us.  The round is split where the blocks that it saves cost more.
 // Split and not: 512 x 1024 x 1024 20.5 and 15.1 us, 1024 x 1024 x 1024 22.1 and 18.5,
@@ -885,7 +902,8 @@ GradPlan plan_of(const dion_grad_source& s) {
   g.whole = (int)(tiles - g.tail);
   g.pad = !rows_aligned16(s.d, s.ldd, 2);
   g.ldd = (n + 7) / 8 * 8;
-  g.parts_bytes = (size_t)g.tail * g.splits * PM * g.bn * 4;
+  // (and behind the parts a word per CTA)
+  g.parts_bytes = g.tail > 0 ? (size_t)g.tail * g.splits * PM * g.bn * 4 + 4 * kMaxCtas : 0;
   g.rows = n >= kRowsColumns && s.kept.tokens >= kRowsTokens;
   g.rows_bytes = g.rows ? up256((size_t)s.kept.tokens * kept_ld(m) * 2) : 0;
   g.pad_bytes = g.pad ? up256((size_t)s.kept.tokens * g.ldd * 2) : 0;
@@ -914,13 +932,11 @@ dion_status check_source(const dion_grad_source& s, int i) {
 
 typedef void (*WgradKernel)(const CUtensorMap, const CUtensorMap, const WgradP);
 dion_status launch(WgradKernel kernel, int threads, int smem, const CUtensorMap& ma, const CUtensorMap& md,
-                   const WgradP& p, int sms, cudaStream_t s) {
+                   const WgradP& p, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return set_error(DION_ERR_CUDA, "k_wgrad: %s", cudaGetErrorString(e));
-  const int64_t units = p.whole + (int64_t)p.tail * p.splits;
-  const int64_t pairs = sms / 2;
-  kernel<<<(unsigned)(2 * (units < pairs ? units : pairs)), threads, smem, s>>>(ma, md, p);
+  kernel<<<(unsigned)p.ctas, threads, smem, s>>>(ma, md, p);
   return launch_status("k_wgrad");
 }
 
@@ -964,6 +980,8 @@ dion_status one_grad(const dion_grad_source& src, int accumulate, char* ws, int3
   p.out = src.G;
   p.parts = reinterpret_cast<float*>(ws);
   p.status = status;
+  p.ctas = 2 * (int)std::min<int64_t>(std::min(sms, kMaxCtas) / 2, g.whole + (int64_t)g.tail * g.splits);
+  p.gave_up = g.tail > 0 ? reinterpret_cast<int32_t*>(ws + g.parts_bytes - 4 * kMaxCtas) : nullptr;
   p.tokens = tokens;
   p.ld_scale = ld / DION_ACT_BLOCK;
   p.ldg = src.ldg;
@@ -980,9 +998,9 @@ dion_status one_grad(const dion_grad_source& src, int accumulate, char* ws, int3
   p.vec = aligned_to(src.G, 32) && src.ldg % 8 == 0;
   p.scale4 = p.ld_scale % 4 == 0 && aligned_to(p.scale, 4);
   p.max_spins = max_spins;
-  const dion_status st = g.rows        ? launch(k_wgrad_rows, RNT, kRowsSmem, mq, md, p, sms, s)
-                         : g.bn == 256 ? launch(k_wgrad<256>, NT, Smem<256>::bytes, mq, md, p, sms, s)
-                                       : launch(k_wgrad<128>, NT, Smem<128>::bytes, mq, md, p, sms, s);
+  const dion_status st = g.rows        ? launch(k_wgrad_rows, RNT, kRowsSmem, mq, md, p, s)
+                         : g.bn == 256 ? launch(k_wgrad<256>, NT, Smem<256>::bytes, mq, md, p, s)
+                                       : launch(k_wgrad<128>, NT, Smem<128>::bytes, mq, md, p, s);
   if (st != DION_OK || g.tail == 0) return st;
   return launch_status("k_wgrad_join", launch_after(k_wgrad_join, dim3((unsigned)(g.bn / 32), PM / 32, (unsigned)g.tail),
                                                     1024, 0, s, p, g.bn));
@@ -991,7 +1009,7 @@ dion_status one_grad(const dion_grad_source& src, int accumulate, char* ws, int3
 }  // namespace
 
 dion_status weight_grad(const dion_grad_source* src, int32_t nsrc, int32_t accumulate, void* ws,
-                        size_t ws_bytes, int32_t* d_status, int64_t max_spins, void* stream) {
+                        size_t ws_bytes, int32_t* d_status, bool clear, int64_t max_spins, void* stream) {
   if (nsrc < 0) return set_error(DION_ERR_INVALID_ARG, "nsources < 0");
   if (nsrc > 0 && !src) return set_error(DION_ERR_INVALID_ARG, "sources is NULL");
   for (int32_t i = 0; i < nsrc; ++i) DION_TRY(check_source(src[i], i));
@@ -1004,6 +1022,9 @@ dion_status weight_grad(const dion_grad_source* src, int32_t nsrc, int32_t accum
     return set_error(DION_ERR_MISALIGNED, "d_status is not 4-byte aligned");
   int sms = 0;
   DION_TRY(check_sm100(&sms));
+  if (clear && nsrc > 0)
+    DION_TRY(launch_status("cudaMemsetAsync", cudaMemsetAsync(d_status, 0, (size_t)nsrc * sizeof(int32_t),
+                                                              reinterpret_cast<cudaStream_t>(stream))));
   for (int32_t i = 0; i < nsrc; ++i)
     DION_TRY(one_grad(src[i], accumulate, static_cast<char*>(ws), d_status ? d_status + i : nullptr,
                       max_spins, sms, reinterpret_cast<cudaStream_t>(stream)));
@@ -1029,7 +1050,7 @@ dion_status dion_weight_grad(const dion_grad_source* sources, int32_t nsources, 
                              void* d_workspace, size_t workspace_bytes, int32_t* d_status,
                              void* stream) {
   return dion::weight_grad(sources, nsources, accumulate, d_workspace, workspace_bytes, d_status,
-                           dion::kDefaultWaitSpins, stream);
+                           false, dion::kDefaultWaitSpins, stream);
 }
 
 }  // extern "C"

@@ -46,7 +46,8 @@ int tc_btp_col_splits(int64_t n);
 cudaError_t tc_update(const void* Pg, int zplane_p, const void* Rg, const void* Qg, bool split,
                       const float* G, float* M, float* X, int count, int64_t m, int64_t n,
                       int64_t r, float mu, float lr_scale, int64_t max_spins, int32_t* flags,
-                      int* tile_counter, float* rmmc, cudaStream_t s, int* nlaunch, bool* done);
+                      const int32_t* held, int* tile_counter, float* rmmc, cudaStream_t s,
+                      int* nlaunch, bool* done);
 // fp32 contractions from three-way bf16 splits: P0 (fp32) and P0s = split(Bs Qs^T),
 // R = Bs^T Ps; K is accumulated in 512-wide chunks added in fp32 registers.
 // (P0s's parts `plane` elements apart, Ps's `zplane_p` matrices apart; 0: count.)

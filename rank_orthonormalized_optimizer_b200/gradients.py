@@ -311,7 +311,7 @@ class WeightGradPlan(_Bound):
     """G = A^T dY of each matrix, from its input A kept in 8 bits (an ActCheckpoint of
     [tokens, m]) and its output's gradient dY (bf16 [tokens, n]); G fp32 [m, n], or with
     ``transposed`` dY^T A, [n, m].  ``status`` (int32, one word per matrix) takes
-    DION_MAT_TIMEOUT where a device wait ran out."""
+    DION_MAT_TIMEOUT where a device wait ran out, and keeps it until it is zeroed."""
 
     def __init__(self, checkpoints, dys, grads, *, transposed=False, workspace=None):
         import torch
@@ -341,7 +341,9 @@ class WeightGradPlan(_Bound):
 class SavedStep(_Bound):
     """A Dion step whose gradients come from kept activations: ``opt`` (a DionB200) and, per
     matrix in the step's order, an ActCheckpoint and dY.  ``step`` forms every gradient in
-    its slot of G and takes the step (dion_step_batched_from_saved)."""
+    its slot of G and takes the step (dion_step_batched_from_saved); a matrix whose gradient ran
+    out of device waits is left alone, and marked DION_MAT_TIMEOUT in ``step``'s status and, until
+    it is zeroed, in ``grad_status``."""
 
     def __init__(self, opt, checkpoints, dys, *, transposed=False, workspace=None):
         import torch
