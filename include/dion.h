@@ -467,7 +467,8 @@ typedef enum dion_dtype { DION_BF16 = 0, DION_FP16 = 1, DION_FP32 = 2 } dion_dty
  * and a byte E, standing for q_i 2^(E - 127).  The exponent is the smallest with
  * max |x_i| <= 448 * 2^(E - 127) (448 is e4m3's largest value), kept within [10, 246];
  * values are rounded to nearest even (2^-4 relative, or 2^-10 * 2^(E - 127) for a block's
- * smallest values).  A block that holds a NaN or an infinity has E = 255 and reads as NaN.
+ * smallest values), and magnitudes above 448 * 2^119 (2.98e38) are cut to that value (by up to
+ * an eighth).  A block that holds a NaN or an infinity has E = 255 and reads as NaN.
  * Every other value is exact in bf16.  e4m3's own NaN bytes (0x7f, 0xff) are never written.
  */
 #define DION_ACT_BLOCK 32

@@ -107,10 +107,11 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) { st_ve
 __device__ __forceinline__ void store8(__half* p, const float* v) { st_vec(p, pack8(v, __half())); }
 
 // ---- 8-bit form: a block of 32 features x_i is e4m3(x_i 2^-e) and the byte e + 127, e the
-// smallest exponent with max|x_i| <= 448 2^e (448 = 1.75 2^8 is e4m3's largest value, so
-// nothing saturates), kept in [-117, 119]: then e4m3's smallest step 2^-9 2^e is a normal
-// bf16 number and 448 2^e is finite, and every value is exact in bf16.  Rounding is to
-// nearest even: half a step of 3 fraction bits, 2^-4 relative, which is what 8 bits cost.
+// smallest exponent with max|x_i| <= 448 2^e (448 = 1.75 2^8 is e4m3's largest value), kept in
+// [-117, 119]: then e4m3's smallest step 2^-9 2^e is a normal bf16 number and 448 2^e is finite,
+// and every value is exact in bf16.  Rounding is to nearest even: half a step of 3 fraction
+// bits, 2^-4 relative, which is what 8 bits cost.  Magnitudes above 448 2^119 (2.98e38, the top
+// quarter of fp32's last binade) are cut to it.
 // A block that holds an infinity or a NaN is marked 255: all of it reads as NaN.
 constexpr uint32_t kInfBits = 0x7f800000u;
 

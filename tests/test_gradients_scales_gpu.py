@@ -79,3 +79,22 @@ def test_scale_bytes_at_any_address(t, m, n, skew):
     """Their neighbours in memory are 255, which would make NaN of what they scale."""
     kept, a = _kept(t, m, [126, 127, 129, 131], 11, skew)
     _check(kept, a, torch.randn(t, n, generator=_gen(4)).bfloat16().cuda(), t, m, n)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("d", [64, 65])
+def test_magnitudes_past_the_form_are_cut(dtype, d):
+    """Above 448 * 2^119 a value reads as that, up to it within half a step; an infinity is NaN."""
+    top = 448.0 * 2.0 ** 119
+    x = torch.zeros(4, d, dtype=dtype, device="cuda")
+    x[0, 3], x[0, 5], x[0, 6] = torch.finfo(dtype).max, -torch.finfo(dtype).max, 1e38
+    x[1, 40], x[1, 41] = top, 3.2e38
+    x[2, 0] = float("inf")
+    kept = dion.ActCheckpoint(4, d)
+    kept.save(x)
+    out = kept.load(torch.empty(4, d, device="cuda")).cpu().double()
+    assert out[0, 3] == top and out[0, 5] == -top and out[1, 40] == top and out[1, 41] == top
+    ref, scale = go.act_round(x.cpu().double().numpy())
+    assert np.array_equal(out.numpy(), ref, equal_nan=True)
+    assert np.array_equal(kept.scale.cpu().numpy(), scale)
+    assert bool(torch.isnan(out[2, :32]).all()) and not out[3].any()
