@@ -397,7 +397,6 @@ struct GradP {
   int64_t sum_ctas;  // CTAs that add up segments; those after them write zeros
   int col_ctas;      // CTAs that share a segment's columns
   int zero_rows;
-  int vec_table;     // rows of the table take 16-byte stores
   float scale;
   int accumulate;
 };
@@ -878,14 +877,14 @@ dion_status embed_grad_impl(const dion_embed_grad* a, void* ws, size_t ws_bytes,
   p.tokens = a->tokens; p.vocab = a->vocab; p.features = a->features;
   p.scale = a->scale;
   p.accumulate = a->accumulate != 0;
-  p.vec_table = a->features % 4 == 0 && rows_aligned16(a->dtable, a->ldt, 4);
   const bool al = a->features % 8 == 0 && rows_vector(a->dtable, a->ldt, 4) && rows_vector(a->dout, a->ldo, es);
   DION_TRY(launch_status("k_embed_sum", a->dtype == DION_BF16   ? launch_sum<__nv_bfloat16>(p, al, g.segs, s)
                                         : a->dtype == DION_FP16 ? launch_sum<__half>(p, al, g.segs, s)
                                                                 : launch_sum<float>(p, al, g.segs, s)));
   if (g.segs > 1) {
     // the list is on the device: a grid that fills the SMs, whose CTAs leave at once without work
-    DION_TRY(launch_status("k_embed_join", launch_after(p.vec_table ? k_embed_join<true> : k_embed_join<false>,
+    const bool v4 = a->features % 4 == 0;  // the pieces in the workspace then start on 16 bytes
+    DION_TRY(launch_status("k_embed_join", launch_after(v4 ? k_embed_join<true> : k_embed_join<false>,
                                                         dim3((unsigned)(sms * 4)), kJoinCols * kJoinGroups, 0, s, p)));
   }
   return DION_OK;
