@@ -364,7 +364,19 @@ class SavedStep(_Bound):
                                                                      opt.num_matrices)
 
     def step(self, X, M, G, Q, lr: float, status=None, accumulate=False, stream=None):
+        import torch
         arr = self.opt._ptrs(X, M, G, Q)
+        for name, ts in (("X", X), ("M", M), ("G", G), ("Q", Q)):
+            for i, t in enumerate(ts):
+                if t.device != self._device:
+                    raise ValueError(f"bucket {i}: {name} is on {t.device}, the checkpoints are on "
+                                     f"{self._device}")
+        if status is not None:
+            if not isinstance(status, torch.Tensor) or status.device != self._device \
+                    or status.dtype != torch.int32 or not status.is_contiguous() \
+                    or status.numel() < self.opt.num_matrices:
+                raise ValueError(f"status must be {self.opt.num_matrices} contiguous int32 words on "
+                                 f"{self._device}")
         _check(dion_step_batched_from_saved(
             self.opt._h, arr, self._arr, len(self.opt.shapes), int(bool(accumulate)), float(lr),
             self._ws, self._ws_bytes,
