@@ -269,9 +269,12 @@ class ActCheckpoint(_Bound):
             ld, one = x.stride()
             if one == 1 and ld >= self.features:
                 return x.data_ptr(), ld, code
-        ptr, ld = self._rows(name, x, self._shape)
-        self._keep.pop()
-        return ptr, ld, _dtype(x)
+        kept = len(self._keep)
+        try:
+            ptr, ld = self._rows(name, x, self._shape)
+            return ptr, ld, _dtype(x)
+        finally:                     # refused or not, x is not kept
+            del self._keep[kept:]
 
     def save(self, x, stream=None):
         """Keep x [tokens, features] (bf16, fp16 or fp32)."""

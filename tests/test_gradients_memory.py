@@ -168,6 +168,19 @@ def test_a_capture_waits_for_nothing_outside(fake):
     assert len(side.waited) == 1
 
 
+def test_a_checkpoint_keeps_no_rows_that_it_is_given(fake):
+    k = dion.ActCheckpoint(64, 32)
+    mine = len(k._keep)
+    for good in (_rows(64, 32), _rows(64, 40)[:, :32].as_subclass(FakeCuda)):
+        k.save(good)
+    for bad in (_rows(63, 32), _rows(64, 32).double().as_subclass(FakeCuda), torch.ones(64, 32),
+                torch.ones(32, 64).as_subclass(FakeCuda).t(), "rows"):
+        for call in (k.save, k.load):
+            with pytest.raises(ValueError):
+                call(bad)
+    assert len(k._keep) == mine
+
+
 # ------------------------------------------------------------------ on the GPU
 @pytest.mark.gpu
 @pytest.mark.parametrize("name", ["embed", "norm", "weight", "act"])
