@@ -110,3 +110,28 @@ def test_marks_are_of_the_call():
     torch.cuda.synchronize()
     assert int(saved.grad_status[0]) == TIMEOUT and not int(status[0]) & TIMEOUT
     assert not torch.equal(X, before) and bool(torch.isfinite(X).all())
+
+
+@pytest.mark.parametrize("r", [16, 272])
+def test_the_step_captured_and_replayed(r):
+    """The words of the call are cleared in each replay, too."""
+    m, n, count = 512, 288, 2
+    kept, dys, X, M, Q = _inputs(900, m, n, count)
+    Q = torch.nn.functional.normalize(torch.randn(count, n, r, generator=torch.Generator().manual_seed(2)),
+                                      dim=1).cuda()
+    G = torch.zeros(count, m, n, device="cuda")
+    opt = dion.DionB200([(count, m, n, r)])
+    saved, status = dion.SavedStep(opt, kept, dys), opt.alloc_status()
+    want, state = [[v.clone() for v in (X, M, Q)] for _ in range(2)]
+    for _ in range(3):
+        saved.step([want[0]], [want[1]], [G], [want[2]], 0.01, status=status)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        saved.step([state[0]], [state[1]], [G], [state[2]], 0.01, status=status)
+    for _ in range(3):
+        status.fill_(-1)
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(state, want):
+        assert torch.equal(a, b)
+    assert not (status & TIMEOUT).any() and not saved.grad_status.any()
