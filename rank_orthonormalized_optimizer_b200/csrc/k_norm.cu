@@ -21,10 +21,11 @@
 // do not start on 16 bytes come as they lie and are read element by element (8192 x 4095 bf16
 // backward 152 us, 789 loaded directly).  Where no ring fits (fp32 backward, more than 8192
 // features) rows are loaded directly, a row per CTA, four rows a CTA up to 512 features.
-// 16384 x 4096 bf16: forward 86 us, kept in 8 bits as well 97, backward 129, which is 6.2 TB/s of
-// the 6.56 that a copy reaches.  A row's barriers cost most where a CTA has its SM for itself, so
-// the backward pass adds a row's last sum and the next row's first ones in one (8192 x 8192 142 us,
-// with a sum for each and two barriers a sum 187; 16384 x 4096 143).  The backward pass keeps each thread's column
+// 16384 x 4096 bf16: forward 87 us, kept in 8 bits as well 97 to 108, backward 129 to 136 in short
+// runs and 148 repeated, which is 5.4 to 6.2 TB/s of the 6.56 that a copy reaches.  A row's barriers
+// cost most where a CTA has its SM for itself, so the backward pass adds a row's last sum and the
+// next row's first ones in one (8192 x 8192 142 us, with a sum for each and two barriers a sum 187;
+// 16384 x 4096 129 and 143; short runs).  The backward pass keeps each thread's column
 // sums over its rows; a second kernel adds the CTAs' sums in a fixed order, so results repeat
 // bit for bit.  All sums are fp32; only the stored rows are rounded.
 #include "operator.h"
@@ -922,7 +923,8 @@ unsigned grad_grid(int64_t tokens, int64_t features) {
   int64_t grid = 0;
   by_width(features, [&](auto nt, auto) {
     constexpr int NT = decltype(nt)::value;
-    // one CTA an SM until each has eight rows: every CTA adds a row of partial sums
+    // every CTA adds a row of partial sums: one CTA an SM up to eight rows for each of these, and
+    // from there on the streaming grid at once (just above, its CTAs have a row or two each)
     const int64_t rows = row_ctas(tokens, NT);
     grid = std::min(rows, rows < 8 * kSms ? (int64_t)kSms : stream_ctas(NT));
   });

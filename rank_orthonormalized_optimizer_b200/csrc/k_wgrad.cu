@@ -8,10 +8,11 @@
 // A's values are exact in bf16 and so are the products in fp32; the only roundings are the
 // fp32 additions.  There are two kernels.  Where G has few columns, k_wgrad reads the 8-bit rows
 // and converts each tile on its way; where it has many, each feature's tile would be converted
-// once for every 256 columns, and the conversion's shared-memory traffic and power take a fifth of
-// the tensor cores' rate (1157 against 1449 TFLOP/s at m = 4096, n = 11008, 16384 tokens): there
-// A is first brought to bf16 rows in the workspace (dion_act_load) and k_wgrad_rows multiplies
-// those.
+// once for every 256 columns, and the conversion's shared-memory traffic and power take a sixth of
+// the tensor cores' rate (m = 4096, n = 11008, 16384 tokens: 1247 us against 1026, 1440 TFLOP/s, in
+// short runs; 1458 against 1237 repeated, under the power cap): there A is first brought to bf16
+// rows in the workspace (dion_act_load) and k_wgrad_rows, whose tensor pipe is 90 % busy,
+// multiplies those.
 //
 // The contraction over the tokens runs on the tensor cores: a persistent pair
 // of CTAs (a cluster, tcgen05 cta_group::2) owns 256 x BN tiles of G, each CTA 128 of the
@@ -27,8 +28,8 @@
 // The tensor cores' accumulation rounds toward zero, which adds up over thousands of MMAs,
 // so the tokens are cut into chunks of kChunk blocks, each accumulated from zero in TMEM
 // (two accumulators in turn), and the epilogue warps add the chunks in fp32 registers: over
-// 16384 like-signed products 3e-7 off (an fp32 product on CUDA cores 6e-7), in k_wgrad at
-// 1227 us for m = 4096, n = 11008; chunks of 8 blocks 1.3e-7 at 1258 us, of 4 8e-8 at 1319 us.
+// 16384 like-signed products 3e-7 off (an fp32 product on CUDA cores 6e-7; chunks of 8 blocks 1.3e-7
+// and 2.5 % slower, of 4 8e-8 and 7 %: k_wgrad at m = 4096, n = 11008 in one run).
 // The tiles that do not fill a last round over all pairs (all of them, in a small matrix) are
 // also split over the tokens, so that every pair has a share; their partial sums go to the
 // workspace and a second kernel adds them in order.  Every wait is bounded; after a give-up the
@@ -864,7 +865,7 @@ constexpr int kMaxCtas = 1024;  // of a launch: k_wgrad_join looks at each with 
 // 32.8; 1024 x 256 x 256 14.4 and 18.5.
 constexpr double kBlockUs = 0.5, kJoinUs = 3, kJoinTileUs = 0.25, kJoinPartUs = 0.03;
 // A is converted beforehand (k_wgrad_rows) from this many columns and tokens on.  Converted first
-// and in the kernel, us: 16384 x 4096 x 11008 1020 and 1277, 8192 x 2048 x 2048 63 and 73,
+// and in the kernel, us: 16384 x 4096 x 11008 1026 and 1247, 8192 x 2048 x 2048 63 and 73,
 // 1024 x 4096 x 4096 54 and 63, 512 x 4096 x 11008 78 and 92; but 16384 x 4096 x 512 101 and 85,
 // 4096 x 1024 x 1024 29 and 27, 200 x 4096 x 4096 46 and 43.
 constexpr int64_t kRowsColumns = 1536, kRowsTokens = 512;
