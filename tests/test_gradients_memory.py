@@ -227,3 +227,49 @@ def test_a_plan_dropped_with_its_call_in_flight(name):
     assert all(j.data_ptr() != where for j in junk)
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("inside", [True, False])
+def test_plans_and_captures(inside):
+    """A plan built inside a capture, and one of before it called on a stream that the capture has
+    forked; both replayed, the second used outside as well."""
+    t, v, d = 2000, 50, 128
+    g = torch.Generator().manual_seed(3)
+    ids, x = torch.randint(-1, v, (t,), generator=g).cuda(), torch.randn(t, d, generator=g).cuda()
+    xb = x.bfloat16()
+    want, out = [(torch.empty(v, d, device="cuda"), torch.empty(d, d, device="cuda")) for _ in range(2)]
+
+    def make(table, G):
+        kept = dion.ActCheckpoint(t, d)
+        return kept, dion.WeightGradPlan([kept], [xb], [G]), dion.EmbedGradPlan(ids, x, table)
+
+    def call(plans, stream=None):
+        plans[0].save(x, stream=stream)
+        plans[1].backward(stream=stream)
+        plans[2].backward(stream=stream)
+
+    call(make(*want))
+    before = make(*out)
+    torch.cuda.synchronize()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        if inside:
+            plans = make(*out)
+            call(plans)
+        else:
+            side.wait_stream(torch.cuda.current_stream())
+            call(before, side)
+            torch.cuda.current_stream().wait_stream(side)
+    for _ in range(2):
+        for o in out:
+            o.fill_(9)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    for o in out:
+        o.fill_(9)
+    side.wait_stream(torch.cuda.current_stream())
+    call(before, side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
